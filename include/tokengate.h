@@ -90,6 +90,13 @@ typedef enum {
 /* Not a timeout: a row index outside [0, N) was given to
  * tg_project_rope_gather; that row was read from row 0 instead. */
 #define TG_STATUS_INDEX_RANGE 0x80u
+/* Not timeouts, set by the 8-bit cache calls (tg_cache_append_q8,
+ * tg_cache_evict_q8, tg_gated_decode_q8): a length outside [0, capacity], or a
+ * count or start outside the cache (it was clamped; rows outside the cache
+ * were not written) ... */
+#define TG_STATUS_CACHE_LENGTH 0x100u
+/* ... and a key or value that is not finite was written into the cache. */
+#define TG_STATUS_CACHE_VALUE 0x200u
 #define TG_STATUS_TIMEOUT_BITS 0x3fu
 
 /* Static description of a status code.  Never NULL. */
@@ -403,6 +410,116 @@ tg_status tg_project_rope_gather(const tg_bf16* h, int64_t N, int32_t d, int64_t
                                  double base, tg_bf16* qkv, int64_t ld_qkv, uint16_t* v16, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ 8-bit KV cache
+ * The keys and values of `batch` sequences held in 8 bits with one scale for
+ * every block of TG_CACHE_BLOCK tokens and KV head (K and V apart): the value
+ * of a code is code * scale.  Next to them, per token, the gate score s (the
+ * logit bias) and w, the attention weight the token has gathered while
+ * decoding.  The calls below append to such a cache, decode over it, evict
+ * from it and read it back.  There is no counterpart on the TokenGate pages
+ * beyond the biased, pruned cache itself (see tg_gated_decode): they print no
+ * cache format and no eviction while decoding.
+ *   format   TG_CACHE_E4M3: codes are fp8 (1-4-3 bits, largest 448, NaN 0x7f);
+ *            TG_CACHE_INT8: two's complement, -127..127.
+ *   scales   powers of two where the library writes them: the least 2^e >=
+ *            2^-126 with amax <= qmax * 2^e (qmax 448 or 127, amax the block's
+ *            largest finite magnitude), so x / scale and code * scale are
+ *            exact, the code is x / scale rounded to nearest even, and a code
+ *            moves to a larger scale by one more rounding only.  tg_cache_read_q8 and
+ *            tg_gated_decode_q8 take any positive finite scale.
+ *   k, v     [batch, capacity, Hkv, d_h] codes; token stride ld_token and
+ *            sequence stride ld_seq in bytes (multiples of 16, heads dense in a
+ *            token), 16-byte aligned.
+ *   lengths  [batch] int32, on the device: the tokens each sequence has.  The
+ *            caller sets and advances them (one array may serve every layer's
+ *            cache); only tg_cache_evict_q8 writes them, in its target.
+ *   s, w     [batch, capacity] fp32 or NULL.
+ * capacity: a multiple of TG_CACHE_BLOCK.  Limits: d_h in {64, 128},
+ * 1 <= Hkv <= 64, 0 <= batch <= 65535, capacity < 2^31 - 2^16.  Rows at or beyond a
+ * sequence's length are never read as keys and never written but by an append.
+ * A length outside [0, capacity] is clamped and flagged (TG_STATUS_CACHE_LENGTH).
+ * The struct itself is read during the call only. */
+#define TG_CACHE_BLOCK 32
+typedef enum { TG_CACHE_E4M3 = 0, TG_CACHE_INT8 = 1 } tg_cache_format;
+typedef struct {
+    int32_t format, batch, Hkv, d_h;
+    int64_t capacity, ld_token, ld_seq;
+    void* k;
+    void* v;
+    float* k_scale; /* [batch, capacity / TG_CACHE_BLOCK, Hkv] */
+    float* v_scale;
+    int32_t* lengths;
+    float* s;
+    float* w;
+} tg_cache_q8;
+
+/* Workspace bytes for the cache calls with n_q queries a sequence of Hq heads
+ * each (n_q = Hq = 0: append, evict and read only; accumulate: whether
+ * tg_gated_decode_q8 will gather weights).  0 for bad arguments.  Zero-fill it
+ * once; concurrent calls must not share one. */
+size_t tg_cache_workspace_bytes(const tg_cache_q8* cache, int32_t n_q, int32_t Hq, int32_t accumulate);
+
+/* Appends counts[b] tokens (n_new where counts is NULL) to every sequence, as
+ * its last ones: token i goes to slot lengths[b] - counts[b] + i, so lengths
+ * hold the tokens AFTER the append (the same array a decode then reads).
+ * k, v: [batch, n_new, Hkv, d_h] bf16, token strides ld_k, ld_v and sequence
+ * strides ld_k_seq, ld_v_seq in elements (multiples of 8), 16-byte aligned.
+ * A block that had tokens already keeps the larger of its scale and the new
+ * tokens' own; where it grows, the codes before it are rounded once more.
+ * s_new: [batch, n_new] fp32 or NULL (bias 0), into cache->s if there is one;
+ * cache->w of the new tokens becomes 0.
+ * +-inf becomes the largest code, NaN the NaN code (int8: 0); either sets
+ * TG_STATUS_CACHE_VALUE and neither counts in amax.  A count outside
+ * [0, n_new] is clamped; tokens whose slot lies outside the cache are not
+ * written (both TG_STATUS_CACHE_LENGTH).  One launch. */
+tg_status tg_cache_append_q8(const tg_cache_q8* cache, const tg_bf16* k, int64_t ld_k, int64_t ld_k_seq,
+                             const tg_bf16* v, int64_t ld_v, int64_t ld_v_seq, int64_t n_new, const int32_t* counts,
+                             const float* s_new, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The values of tokens [first, first + n) of every sequence, code * scale
+ * rounded to bf16 (exact where the scale is a power of two), into k_out and
+ * v_out [batch, n, Hkv, d_h] dense, 16-byte aligned -- the layout tg_gated_decode
+ * takes.  Rows at or beyond a sequence's length are left as they were.  One launch. */
+tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, tg_bf16* k_out, tg_bf16* v_out,
+                           void* stream);
+
+/* Decoding step of token-gated attention over the cache, n_q new tokens a
+ * sequence (their own keys appended before the call): query i of sequence b
+ * sees the keys c < T_i = lengths[b] - (n_q - 1 - i),
+ *   l_c = tau * (q_h . k_{c,kv(h)}) / sqrt(d_h) + gain_h * s_c,   c < T_i
+ *   out_h = sum_c softmax_c(l_c) v_{c,kv(h)},   kv(h) = h / (Hq / Hkv)
+ * and, with accumulate, cache->w[b, c] += sum over i and h of softmax_c(l_c).
+ * A query that sees no key, or none with l_c > -inf, gets out 0 and lse -inf and
+ * adds no weight.  Keys with s_c = -inf are masked for heads of positive gain.
+ * q, out: [batch, n_q, Hq, d_h] bf16 dense, 16-byte aligned; lse: [batch, n_q,
+ * Hq] fp32 or NULL.  The bias is 0 where cache->s or gain is NULL.
+ * max_len: an upper bound on lengths that sizes the launch (0 = capacity);
+ * a longer sequence is still read whole, by fewer thread blocks.
+ * Supported: Hq a multiple of Hkv, n_q * Hq / Hkv <= 16, tau finite.  One launch,
+ * a second one with accumulate.  Every code is read once (HBM-bound); logits, softmax
+ * and sums in fp32, the products on the tensor cores from the codes in fp16
+ * (exact) with q scaled by a power of two to fp16 and the softmax's weights
+ * rounded to fp16.  Deterministic. */
+tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16* q, int32_t n_q, int32_t Hq, const float* gain,
+                             float tau, int32_t accumulate, int64_t max_len, tg_bf16* out, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction by gathered attention weight: copies what stays of each sequence of
+ * src into dst (another cache of the same format, batch, Hkv and d_h, of
+ * capacity >= budget, sharing no memory with src) in ascending slot order.
+ * A sequence of n <= budget tokens stays whole; else its first `sink` and last
+ * `recent` tokens stay and, of those between, the budget - sink - recent of
+ * largest w (lower slot first on ties, -0 == +0, NaN below every number).
+ * Blocks of dst get scales of their own from the values they receive, as an
+ * append would give them.  s and w move with their tokens (where both caches have
+ * them); dst->lengths[b] = min(n, budget); kept: [batch, budget] int32, the slots
+ * in src, -1 behind the last.  src->w must not be NULL; sink + recent <= budget.
+ * max_len: an upper bound on src->lengths that sizes the launch (0 = capacity).
+ * Two launches; rows of dst behind its new lengths are left as they were. */
+tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8* dst, int64_t budget, int64_t sink,
+                            int64_t recent, int64_t max_len, int32_t* kept, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* Test hook (fault injection without a fault): sets the time limit of the
  * grid barrier inside tg_topk_select, tg_topk_select_noalloc and
  * tg_random_select on the current device to `ns` nanoseconds of %globaltimer
@@ -424,7 +541,8 @@ tg_status tg_debug_set_cta_pairs(int enabled);
 /* Reads the workspace's status word after synchronizing `stream`.
  * *status_word receives the raw TG_STATUS_* bits (may be NULL).
  * Returns TG_ERR_TIMEOUT if a timeout bit is set, else TG_ERR_RANGE if
- * TG_STATUS_V_RANGE or TG_STATUS_INDEX_RANGE is set, TG_OK otherwise. */
+ * TG_STATUS_V_RANGE, TG_STATUS_INDEX_RANGE, TG_STATUS_CACHE_LENGTH or
+ * TG_STATUS_CACHE_VALUE is set, TG_OK otherwise. */
 tg_status tg_device_status(const void* workspace, uint32_t* status_word, void* stream);
 
 #ifdef __cplusplus

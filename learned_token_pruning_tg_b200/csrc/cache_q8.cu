@@ -1,0 +1,608 @@
+// cache_q8.cu -- the 8-bit KV cache's own calls: append, read back, evict.
+//
+// A block is 32 tokens of one head (K and V apart) under one scale 2^e, the least with amax <= qmax 2^e.
+// Every kernel here moves bytes: one warp holds one block in registers, so the largest magnitude is a
+// warp reduction and the block is read and written once.
+//
+// append: bf16 rows (2 rows a warp load, 16 bytes a lane) -> codes (8 bytes a lane).  A block with tokens of an
+//   earlier append keeps the larger scale; its codes move to it by one multiplication with a power
+//   of two and one rounding.
+// evict: a cluster of thread blocks finds a sequence's kept slots by a radix select over the weights
+//   (11 + 11 + 10 bits of the order-preserving key, counts merged through distributed shared memory), then one
+//   warp per new block gathers its 32 rows.
+#include "tg_cache.cuh"
+
+namespace tg {
+namespace q8 {
+
+constexpr int kWarps = 8;                // warps of an append, read or gather thread block
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// ------------------------------------------------------------------------------------------- append
+struct AppendArgs {
+    Cache c;
+    const __nv_bfloat16 *k, *v;
+    int64_t ld_k, ld_k_seq, ld_v, ld_v_seq;
+    int64_t n_new;
+    const int32_t* counts;
+    const float* s_new;
+    unsigned int* status;
+    int units;                           // blocks a sequence's new tokens may touch * Hkv * 2
+};
+
+// One warp: block j of one head of K or V.  Rows [first, last) of the block are new (their tokens start at
+// `x`), rows before them stay.
+template <int D, int FMT>
+__device__ __forceinline__ void append_block(const __nv_bfloat16* x, int64_t ld, uint8_t* codes, int64_t ld_token,
+                                             float* scale, int first, int last, unsigned int* status) {
+    constexpr int LPR = D / 8;           // lanes of a row (8 elements, 16 bytes each)
+    constexpr int RPL = 32 / LPR;        // rows a warp load covers
+    constexpr int N = kBlock / RPL;
+    const int lane = threadIdx.x & 31, row0 = lane / LPR, col = (lane % LPR) * 8;
+    uint4 u[N];
+    uint32_t top = 0;                    // the largest magnitudes, as bf16 bits in either half
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = i * RPL + row0;
+        u[i] = (r >= first && r < last) ? __ldg(reinterpret_cast<const uint4*>(x + (r - first) * ld + col))
+                                        : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        top = __vmaxu2(top, u[i].x & 0x7fff7fffu);
+        top = __vmaxu2(top, u[i].y & 0x7fff7fffu);
+        top = __vmaxu2(top, u[i].z & 0x7fff7fffu);
+        top = __vmaxu2(top, u[i].w & 0x7fff7fffu);
+    }
+    uint32_t bits = max(top & 0xffffu, top >> 16);
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    const bool odd = bits >= 0x7f80u;    // an infinity or a NaN: the largest finite magnitude instead
+    if (odd) {
+        bits = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+                if (lo < 0x7f80u) bits = max(bits, lo);
+                if (hi < 0x7f80u) bits = max(bits, hi);
+            }
+        }
+        bits = __reduce_max_sync(0xffffffffu, bits);
+        if (lane == 0) atomicOr(status, TG_STATUS_CACHE_VALUE);
+    }
+    float sc = scale_for<FMT>(__uint_as_float(bits << 16));
+    if (first > 0) {
+        const float before = *scale;
+        if (before >= sc) {
+            sc = before;
+        } else if (before > 0.0f) {      // (codes without a scale that is a number stand for nothing: they stay)
+            // the scale grows: the block's earlier codes once more
+            const float ratio = __fdiv_rn(before, sc);
+            constexpr int LPC = D / 16;  // lanes of a row of codes (16 bytes each)
+            for (int r = lane / LPC; r < first; r += 32 / LPC) {
+                uint4* p = reinterpret_cast<uint4*>(codes + r * ld_token + (lane % LPC) * 16);
+                const uint4 c = *p;
+                uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f[4];
+                    decode4<FMT>(w[j], f);
+                    w[j] = encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+                }
+                *p = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncwarp();                    // every lane has read the scale
+    }
+    if (lane == 0) *scale = sc;
+    const float inv = __fdiv_rn(1.0f, sc);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = i * RPL + row0;
+        if (r < first || r >= last) continue;
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
+        }
+        if (FMT == TG_CACHE_INT8 && odd) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] != f[j] ? 0.0f : fminf(fmaxf(f[j], -127.0f), 127.0f);
+        }
+        *reinterpret_cast<uint2*>(codes + r * ld_token + col) =
+            make_uint2(encode4<FMT>(f[0], f[1], f[2], f[3]), encode4<FMT>(f[4], f[5], f[6], f[7]));
+    }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) cache_append_q8_kernel(const AppendArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (unit >= a.units) return;
+    const int b = blockIdx.y, Hkv = a.c.Hkv;
+    // K's heads, then V's, then the next block
+    const int head = unit % Hkv, is_v = unit / Hkv % 2, blk = unit / (2 * Hkv);
+    const int64_t len = __ldg(a.c.lengths + b);
+    int64_t count = a.n_new;
+    bool bad = len < 0 || len > a.c.capacity;
+    if (a.counts) {
+        const int64_t given = __ldg(a.counts + b);
+        count = given < 0 ? 0 : (given > a.n_new ? a.n_new : given);
+        bad = bad || count != given;
+    }
+    const int64_t start = len - count;   // token i goes to slot start + i
+    bad = bad || (count > 0 && start < 0);
+    if (bad && unit == 0 && lane == 0) atomicOr(a.status, TG_STATUS_CACHE_LENGTH);
+    const int64_t lo = start < 0 ? 0 : start, hi = len < a.c.capacity ? len : a.c.capacity;
+    const int64_t j = lo / kBlock + blk, s0 = j * kBlock;
+    if (lo >= hi || s0 >= hi) return;    // no new token in this block
+    const int first = lo > s0 ? static_cast<int>(lo - s0) : 0;
+    const int last = hi - s0 < kBlock ? static_cast<int>(hi - s0) : kBlock;
+    const int64_t token = s0 + first - start;   // the first of them
+    const __nv_bfloat16* x = is_v ? a.v + b * a.ld_v_seq + token * a.ld_v : a.k + b * a.ld_k_seq + token * a.ld_k;
+    uint8_t* codes = (is_v ? a.c.v : a.c.k) + b * a.c.ld_seq + s0 * a.c.ld_token + head * D;
+    float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (b * a.c.blocks() + j) * Hkv + head;
+    append_block<D, FMT>(x + static_cast<int64_t>(head) * D, is_v ? a.ld_v : a.ld_k, codes, a.c.ld_token, scale, first,
+                         last, a.status);
+    if (head == 0 && !is_v && lane >= first && lane < last) {
+        const int64_t at = b * a.c.capacity + s0 + lane;
+        if (a.c.s) a.c.s[at] = a.s_new ? __ldg(a.s_new + b * a.n_new + token + lane - first) : 0.0f;
+        if (a.c.w) a.c.w[at] = 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------------------------------- read
+struct ReadArgs {
+    Cache c;
+    int64_t first, n;
+    __nv_bfloat16 *k, *v;
+};
+
+// One thread: 16 codes of one token and head, K or V, to 32 bytes.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.y;
+    int64_t len = __ldg(a.c.lengths + b);
+    if (len > a.c.capacity) len = a.c.capacity;
+    const int64_t rows = (len < a.first + a.n ? len : a.first + a.n) - a.first;
+    const int per_row = a.c.Hkv * (D / 16);
+    const int64_t total = rows * per_row;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t row = i / per_row;
+        const int u = static_cast<int>(i - row * per_row), head = u / (D / 16), col = u % (D / 16) * 16;
+        const int64_t slot = a.first + row;
+        const int64_t from = b * a.c.ld_seq + slot * a.c.ld_token + head * D + col;
+        const int64_t to = ((b * a.n + row) * a.c.Hkv + head) * D + col;
+        const int64_t sc = (b * a.c.blocks() + slot / kBlock) * a.c.Hkv + head;
+        const uint4 ck = __ldg(reinterpret_cast<const uint4*>(a.c.k + from));
+        const uint4 cv = __ldg(reinterpret_cast<const uint4*>(a.c.v + from));
+        const float sk = __ldg(a.c.k_scale + sc), sv = __ldg(a.c.v_scale + sc);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint4 c = x ? cv : ck;
+            const float s = x ? sv : sk;
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f[4];
+                decode4<FMT>(w[j], f);
+                o[2 * j] = pack_bf16x2(f[0] * s, f[1] * s);
+                o[2 * j + 1] = pack_bf16x2(f[2] * s, f[3] * s);
+            }
+            uint4* p = reinterpret_cast<uint4*>((x ? a.v : a.k) + to);
+            p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------- evict
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kCluster = 8;              // thread blocks that select for one sequence
+
+struct EvictArgs {
+    Cache src, dst;
+    int64_t budget, sink, recent;
+    int32_t* kept;
+    unsigned int* status;
+    int cached;                          // keys of a thread block that fit its shared memory
+};
+
+__device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+    return v;
+}
+
+// Exclusive scan over the block of one value per thread; *total is the block's sum.
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* s_warp, unsigned* total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        unsigned w = s_warp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        s_warp[lane] = w;
+    }
+    __syncthreads();
+    const unsigned before = (warp ? s_warp[warp - 1] : 0u) + incl - v;
+    *total = s_warp[kSelWarps - 1];
+    __syncthreads();
+    return before;
+}
+
+// One cluster per sequence: kept[b, :] ascending, dst's length.  Each thread block owns a contiguous
+// eighth of the tokens between the sinks and the recent ones (keys in shared memory where they fit, else read again
+// from L2 each pass), each warp a contiguous part of that.
+__global__ void __launch_bounds__(kSelThreads, 1) __cluster_dims__(kCluster, 1, 1)
+cache_evict_select_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t s_key[];
+    __shared__ unsigned s_hist[3][2048];  // one a pass, so that a peer may still read the last one
+    __shared__ unsigned s_warp[kSelWarps];
+    __shared__ unsigned s_pick[2], s_cnt[2], s_before[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank_in();
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.y;
+    const int n = length_of(a.src, b, a.status);
+    int32_t* kept = a.kept + b * a.budget;
+    const int gtid = rank * kSelThreads + tid, gthreads = kCluster * kSelThreads;
+    if (gtid == 0) a.dst.lengths[b] = static_cast<int32_t>(n < a.budget ? n : a.budget);
+    if (n <= a.budget) {                 // the whole cluster: nothing leaves
+        for (int64_t i = gtid; i < a.budget; i += gthreads) kept[i] = i < n ? static_cast<int32_t>(i) : -1;
+        return;
+    }
+    const int sink = static_cast<int>(a.sink), recent = static_cast<int>(a.recent);
+    const int budget = static_cast<int>(a.budget), kd = budget - sink - recent;
+    for (int i = gtid; i < sink; i += gthreads) kept[i] = i;
+    for (int i = gtid; i < recent; i += gthreads) kept[budget - recent + i] = n - recent + i;
+    if (kd == 0) return;
+
+    // this block's span [c0, c1) and this warp's part of it
+    const int m = n - sink - recent;
+    const int per = (m + kCluster - 1) / kCluster;
+    const int c0 = min(static_cast<int>(rank) * per, m), c1 = min(c0 + per, m), cn = c1 - c0;
+    const int wper = ((per + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int w0 = min(warp * wper, cn), w1 = min(w0 + wper, cn);
+    const float* w = a.src.w + b * a.src.capacity + sink + c0;
+    const bool cached = per <= a.cached;
+    auto key_at = [&](int i) { return cached ? s_key[i] : radix_key(__ldcg(w + i)); };
+
+    uint32_t prefix = 0, pmask = 0;
+    unsigned krem = static_cast<unsigned>(kd);   // rank of the threshold among the keys that match `prefix`
+    for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
+    __syncthreads();
+#pragma unroll 1
+    for (int p = 0; p < 3; ++p) {
+        const int shift = p == 0 ? 21 : (p == 1 ? 10 : 0), nb = p == 2 ? 1024 : 2048;
+        for (int i0 = 0; i0 < cn; i0 += kSelThreads) {
+            const int i = i0 + tid;
+            uint32_t key = 0;
+            if (i < cn) {
+                if (p == 0) {
+                    key = radix_key(__ldcg(w + i));
+                    if (cached) s_key[i] = key;
+                } else {
+                    key = key_at(i);
+                }
+            }
+            const bool match = i < cn && (key & pmask) == prefix;
+            const unsigned active = __ballot_sync(0xffffffffu, match);
+            if (match) {
+                const uint32_t digit = (key >> shift) & (nb - 1);
+                const unsigned peers = __match_any_sync(active, digit);
+                if (lane == __ffs(peers) - 1) atomicAdd(&s_hist[p][digit], static_cast<unsigned>(__popc(peers)));
+            }
+        }
+        cluster_sync_all();
+        // every thread block sums the whole histogram: two bins a thread, from the top digit down
+        unsigned c[2] = {0u, 0u};
+        const int d0 = nb - 1 - 2 * tid;
+        if (d0 > 0) {
+            uint32_t x[2][kCluster];
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                x[0][r] = cluster_ld(&s_hist[p][d0], r);
+                x[1][r] = cluster_ld(&s_hist[p][d0 - 1], r);
+            }
+#pragma unroll
+            for (int r = 0; r < kCluster; ++r) {
+                c[0] += x[0][r];
+                c[1] += x[1][r];
+            }
+        }
+        unsigned tot;
+        const unsigned e = block_scan(c[0] + c[1], s_warp, &tot);
+        if (e < krem && krem <= e + c[0]) {
+            s_pick[0] = d0;
+            s_pick[1] = e;
+        } else if (e + c[0] < krem && krem <= e + c[0] + c[1]) {
+            s_pick[0] = d0 - 1;
+            s_pick[1] = e + c[0];
+        }
+        __syncthreads();
+        prefix |= s_pick[0] << shift;
+        pmask |= static_cast<uint32_t>(nb - 1) << shift;
+        krem -= s_pick[1];
+        __syncthreads();
+    }
+    // keys above the threshold `prefix` stay, and the first krem equal to it
+    unsigned gt = 0, eq = 0;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const uint32_t key = i0 + lane < w1 ? key_at(i0 + lane) : 0u;
+        const bool in = i0 + lane < w1;
+        gt += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
+        eq += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+    }
+    unsigned gt_all, eq_all;
+    unsigned gt_before = block_scan(lane == 0 ? gt : 0u, s_warp, &gt_all);
+    unsigned eq_before = block_scan(lane == 0 ? eq : 0u, s_warp, &eq_all);
+    if (tid == 0) {
+        s_cnt[0] = gt_all;
+        s_cnt[1] = eq_all;
+    }
+    cluster_sync_all();
+    if (warp == 0) {
+        unsigned x = 0, y = 0;
+        if (lane < static_cast<int>(rank)) {
+            x = cluster_ld(&s_cnt[0], lane);
+            y = cluster_ld(&s_cnt[1], lane);
+        }
+        x = __reduce_add_sync(0xffffffffu, x);
+        y = __reduce_add_sync(0xffffffffu, y);
+        if (lane == 0) {
+            s_before[0] = x;
+            s_before[1] = y;
+        }
+    }
+    __syncthreads();
+    gt_before = __shfl_sync(0xffffffffu, gt_before, 0) + s_before[0];
+    eq_before = __shfl_sync(0xffffffffu, eq_before, 0) + s_before[1];
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const bool in = i0 + lane < w1;
+        const uint32_t key = in ? key_at(i0 + lane) : 0u;
+        const unsigned mg = __ballot_sync(0xffffffffu, in && key > prefix);
+        const unsigned me = __ballot_sync(0xffffffffu, in && key == prefix);
+        const unsigned below = (1u << lane) - 1u;
+        const unsigned g = gt_before + __popc(mg & below), q = eq_before + __popc(me & below);
+        const bool keep = in && (key > prefix || (key == prefix && q < krem));
+        if (keep) kept[sink + g + min(q, krem)] = sink + c0 + i0 + lane;
+        gt_before += __popc(mg);
+        eq_before += __popc(me);
+    }
+    cluster_sync_all();                  // no block leaves while a peer may read its shared memory
+}
+
+// One warp: one new block of one head, K or V.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const EvictArgs a) {
+    constexpr int LPR = D / 16;          // lanes of a row of codes
+    constexpr int RPL = 32 / LPR;
+    constexpr int N = kBlock / RPL;
+    pdl_wait();
+    pdl_trigger();
+    const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int Hkv = a.src.Hkv, head = unit % Hkv, is_v = unit / Hkv % 2;
+    const int64_t j = unit / (2 * Hkv), b = blockIdx.y;
+    if (j * kBlock >= a.budget) return;
+    const int slot = j * kBlock + lane < a.budget ? a.kept[b * a.budget + j * kBlock + lane] : -1;
+    if (!__any_sync(0xffffffffu, slot >= 0)) return;
+    const uint8_t* from = (is_v ? a.src.v : a.src.k) + b * a.src.ld_seq + head * D + (lane % LPR) * 16;
+    const float* from_scale = (is_v ? a.src.v_scale : a.src.k_scale) + b * a.src.blocks() * Hkv + head;
+    const float mine = slot >= 0 ? __ldg(from_scale + static_cast<int64_t>(slot / kBlock) * Hkv) : 0.0f;
+    uint4 u[N];
+    float sc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = i * RPL + lane / LPR;
+        const int at = __shfl_sync(0xffffffffu, slot, r);
+        sc[i] = __shfl_sync(0xffffffffu, mine, r);
+        u[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(from + at * a.src.ld_token)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // the largest magnitude of a row's codes: their own order (NaN codes do not count)
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            uint32_t c;
+            if constexpr (FMT == TG_CACHE_E4M3) {
+                c = w[x] & 0x7f7f7f7fu;
+                c &= ~__vcmpeq4(c, 0x7f7f7f7fu);
+            } else {
+                c = __vabs4(w[x]);
+            }
+            top = __vmaxu4(top, c);
+        }
+        top = __vmaxu4(top, top >> 16);
+        top = __vmaxu4(top, top >> 8) & 0xffu;
+        float f[4];
+        if constexpr (FMT == TG_CACHE_E4M3)
+            decode4<FMT>(top, f);
+        else
+            f[0] = static_cast<float>(top);
+        amax = fmaxf(amax, f[0] * sc[i]);
+    }
+    const float scale = scale_for<FMT>(warp_max(amax));
+    uint8_t* to = (is_v ? a.dst.v : a.dst.k) + b * a.dst.ld_seq + j * kBlock * a.dst.ld_token + head * D +
+                  (lane % LPR) * 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int r = i * RPL + lane / LPR;
+        const int at = __shfl_sync(0xffffffffu, slot, r);
+        uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        if (sc[i] != scale) {
+            const float ratio = __fdiv_rn(sc[i], scale);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float f[4];
+                decode4<FMT>(w[x], f);
+                w[x] = encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+            }
+        }
+        if (at >= 0) *reinterpret_cast<uint4*>(to + r * a.dst.ld_token) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (lane == 0) (is_v ? a.dst.v_scale : a.dst.k_scale)[(b * a.dst.blocks() + j) * Hkv + head] = scale;
+    if (head == 0 && !is_v && slot >= 0) {
+        const int64_t at = b * a.dst.capacity + j * kBlock + lane, of = b * a.src.capacity + slot;
+        if (a.dst.s && a.src.s) a.dst.s[at] = a.src.s[of];
+        if (a.dst.w) a.dst.w[at] = a.src.w[of];
+    }
+}
+
+// Whether [p, p + bytes) and [q, q + more) share memory.
+static bool overlap(const void* p, size_t bytes, const void* q, size_t more) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return p && q && x < y + more && y < x + bytes;
+}
+static size_t code_bytes(const Cache& c, int d) {
+    if (c.batch == 0 || c.capacity == 0) return 0;
+    return static_cast<size_t>(c.batch - 1) * c.ld_seq + static_cast<size_t>(c.capacity - 1) * c.ld_token +
+           static_cast<size_t>(c.Hkv) * d;
+}
+
+}  // namespace q8
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" tg_status tg_cache_append_q8(const tg_cache_q8* cache, const tg_bf16* k, int64_t ld_k, int64_t ld_k_seq,
+                                        const tg_bf16* v, int64_t ld_v, int64_t ld_v_seq, int64_t n_new,
+                                        const int32_t* counts, const float* s_new, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    q8::AppendArgs a = {};
+    const tg_status ok = q8::check_cache(cache, &a.c);
+    if (ok != TG_OK) return ok;
+    if (n_new < 0) return TG_ERR_INVALID_ARG;
+    if (n_new > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    if (n_new == 0 || a.c.batch == 0 || a.c.capacity == 0) return TG_OK;
+    if (!k || !v || !workspace || !aligned16(k) || !aligned16(v) || !aligned16(workspace)) return TG_ERR_INVALID_ARG;
+    if (workspace_bytes < kWsHeader) return TG_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(a.c.Hkv) * cache->d_h;
+    if (((ld_k | ld_v | ld_k_seq | ld_v_seq) % 8) != 0) return TG_ERR_INVALID_ARG;
+    if (n_new > 1 && (ld_k < row || ld_v < row)) return TG_ERR_INVALID_ARG;
+    if (a.c.batch > 1 && (ld_k_seq < row || ld_v_seq < row)) return TG_ERR_INVALID_ARG;
+    a.k = reinterpret_cast<const __nv_bfloat16*>(k);
+    a.v = reinterpret_cast<const __nv_bfloat16*>(v);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.ld_k_seq = ld_k_seq;
+    a.ld_v_seq = ld_v_seq;
+    a.n_new = n_new;
+    a.counts = counts;
+    a.s_new = s_new;
+    a.status = status_word(workspace);
+    // blocks that n tokens in a row touch at most, wherever they begin
+    int64_t blocks = (n_new + q8::kBlock - 2) / q8::kBlock + 1;
+    const int64_t all = a.c.capacity / q8::kBlock;
+    if (blocks > all) blocks = all;
+    const int64_t units = blocks * a.c.Hkv * 2;
+    if (units > 0x7fffff00LL) return TG_ERR_UNSUPPORTED;
+    a.units = static_cast<int>(units);
+    const dim3 grid(static_cast<unsigned>((units + q8::kWarps - 1) / q8::kWarps), static_cast<unsigned>(a.c.batch));
+    auto kern = cache->d_h == 128
+                    ? (cache->format == TG_CACHE_E4M3 ? q8::cache_append_q8_kernel<128, TG_CACHE_E4M3>
+                                                      : q8::cache_append_q8_kernel<128, TG_CACHE_INT8>)
+                    : (cache->format == TG_CACHE_E4M3 ? q8::cache_append_q8_kernel<64, TG_CACHE_E4M3>
+                                                      : q8::cache_append_q8_kernel<64, TG_CACHE_INT8>);
+    return q8::launch_pdl(kern, grid, dim3(q8::kWarps * 32), 0, as_stream(stream), a);
+}
+
+extern "C" tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, tg_bf16* k_out,
+                                      tg_bf16* v_out, void* stream) {
+    q8::ReadArgs a = {};
+    const tg_status ok = q8::check_cache(cache, &a.c);
+    if (ok != TG_OK) return ok;
+    if (first < 0 || n < 0 || first > a.c.capacity || n > a.c.capacity - first) return TG_ERR_INVALID_ARG;
+    if (n == 0 || a.c.batch == 0) return TG_OK;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return TG_ERR_INVALID_ARG;
+    a.first = first;
+    a.n = n;
+    a.k = reinterpret_cast<__nv_bfloat16*>(k_out);
+    a.v = reinterpret_cast<__nv_bfloat16*>(v_out);
+    int64_t blocks = (n * a.c.Hkv * (cache->d_h / 16) + q8::kWarps * 32 - 1) / (q8::kWarps * 32);
+    if (blocks > (1 << 20)) blocks = 1 << 20;   // the rest by the kernel's stride
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.c.batch));
+    auto kern = cache->d_h == 128 ? (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<128, TG_CACHE_E4M3>
+                                                                    : q8::cache_read_q8_kernel<128, TG_CACHE_INT8>)
+                                  : (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<64, TG_CACHE_E4M3>
+                                                                    : q8::cache_read_q8_kernel<64, TG_CACHE_INT8>);
+    return q8::launch_pdl(kern, grid, dim3(q8::kWarps * 32), 0, as_stream(stream), a);
+}
+
+extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8* dst, int64_t budget, int64_t sink,
+                                       int64_t recent, int64_t max_len, int32_t* kept, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    q8::EvictArgs a = {};
+    tg_status ok = q8::check_cache(src, &a.src);
+    if (ok == TG_OK) ok = q8::check_cache(dst, &a.dst);
+    if (ok != TG_OK) return ok;
+    if (src->format != dst->format || src->batch != dst->batch || src->Hkv != dst->Hkv || src->d_h != dst->d_h)
+        return TG_ERR_INVALID_ARG;
+    if (budget < 0 || sink < 0 || recent < 0 || max_len < 0 || sink > budget || recent > budget - sink ||
+        budget > dst->capacity)
+        return TG_ERR_INVALID_ARG;
+    if (src->batch == 0) return TG_OK;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < kWsHeader || (budget > 0 && !kept) ||
+        (src->capacity > 0 && !src->w))
+        return TG_ERR_INVALID_ARG;
+    const size_t sb = q8::code_bytes(a.src, src->d_h), db = q8::code_bytes(a.dst, dst->d_h);
+    const size_t ss = static_cast<size_t>(src->batch) * src->capacity * 4;
+    const size_t ds = static_cast<size_t>(dst->batch) * dst->capacity * 4;
+    if (q8::overlap(src->k, sb, dst->k, db) || q8::overlap(src->v, sb, dst->v, db) ||
+        q8::overlap(src->k, sb, dst->v, db) || q8::overlap(src->v, sb, dst->k, db) ||
+        q8::overlap(src->w, ss, dst->w, ds) || q8::overlap(src->s, ss, dst->s, ds) || src->k_scale == dst->k_scale ||
+        src->v_scale == dst->v_scale || src->lengths == dst->lengths)
+        return TG_ERR_INVALID_ARG;
+    a.budget = budget;
+    a.sink = sink;
+    a.recent = recent;
+    a.kept = kept;
+    a.status = status_word(workspace);
+    if (max_len == 0 || max_len > src->capacity) max_len = src->capacity;
+    // keys of a thread block in its shared memory (beside 25 KB of histograms) where they fit
+    constexpr int kMostCached = 48 * 1024;
+    int64_t per = (max_len + q8::kCluster - 1) / q8::kCluster;
+    a.cached = per <= kMostCached ? static_cast<int>(per) : 0;
+    static std::atomic<int> smem_set[64];
+    if (!set_max_dynamic_smem(q8::cache_evict_select_kernel, kMostCached * 4, smem_set)) return TG_ERR_CUDA;
+    cudaStream_t st = as_stream(stream);
+    tg_status r = q8::launch_pdl(q8::cache_evict_select_kernel, dim3(q8::kCluster, static_cast<unsigned>(src->batch)),
+                                 dim3(q8::kSelThreads), static_cast<size_t>(a.cached) * 4, st, a);
+    if (r != TG_OK || budget == 0) return r;
+    const int64_t units = (budget + q8::kBlock - 1) / q8::kBlock * src->Hkv * 2;
+    const dim3 grid(static_cast<unsigned>((units + q8::kWarps - 1) / q8::kWarps), static_cast<unsigned>(src->batch));
+    auto kern = src->d_h == 128 ? (src->format == TG_CACHE_E4M3 ? q8::cache_evict_gather_kernel<128, TG_CACHE_E4M3>
+                                                                : q8::cache_evict_gather_kernel<128, TG_CACHE_INT8>)
+                                : (src->format == TG_CACHE_E4M3 ? q8::cache_evict_gather_kernel<64, TG_CACHE_E4M3>
+                                                                : q8::cache_evict_gather_kernel<64, TG_CACHE_INT8>);
+    return q8::launch_pdl(kern, grid, dim3(q8::kWarps * 32), 0, st, a);
+}

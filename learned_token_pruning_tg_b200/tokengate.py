@@ -22,8 +22,20 @@ TG_OP_GATE, TG_OP_SELECT, TG_OP_ATTENTION, TG_OP_ALL, TG_OP_DECODE, TG_OP_ATTENT
 TG_STATUS_SELECT_TIMEOUT, TG_STATUS_GATE_TIMEOUT, TG_STATUS_ATTENTION_TIMEOUT, TG_STATUS_DECODE_TIMEOUT = 1, 2, 4, 8
 TG_STATUS_BACKWARD_TIMEOUT, TG_STATUS_PROJECT_TIMEOUT, TG_STATUS_V_RANGE = 16, 32, 64
 TG_STATUS_INDEX_RANGE = 128
+TG_STATUS_CACHE_LENGTH, TG_STATUS_CACHE_VALUE = 256, 512
+TG_CACHE_E4M3, TG_CACHE_INT8 = range(2)
+TG_CACHE_BLOCK = 32
 
 _lib = None
+
+
+class CacheStruct(ctypes.Structure):
+    """tg_cache_q8 of the C header."""
+    _fields_ = [("format", ctypes.c_int32), ("batch", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d_h", ctypes.c_int32),
+                ("capacity", ctypes.c_int64), ("ld_token", ctypes.c_int64), ("ld_seq", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("s", ctypes.c_void_p),
+                ("w", ctypes.c_void_p)]
 
 
 class TokenGateError(RuntimeError):
@@ -69,6 +81,13 @@ def lib() -> ctypes.CDLL:
                                              sz, vp]
         L.tg_gated_attention_backward.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, vp, vp, f32, vp,
                                                   vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        cq = ctypes.POINTER(CacheStruct)
+        L.tg_cache_workspace_bytes.argtypes = [cq, i32, i32, i32]
+        L.tg_cache_workspace_bytes.restype = sz
+        L.tg_cache_append_q8.argtypes = [cq, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+        L.tg_cache_read_q8.argtypes = [cq, i64, i64, vp, vp, vp]
+        L.tg_gated_decode_q8.argtypes = [cq, vp, i32, i32, vp, f32, i32, i64, vp, vp, vp, sz, vp]
+        L.tg_cache_evict_q8.argtypes = [cq, cq, i64, i64, i64, i64, vp, vp, sz, vp]
         L.tg_debug_set_select_wait_limit.argtypes = [ctypes.c_uint64]
         L.tg_debug_set_cta_pairs.argtypes = [ctypes.c_int]
         L.tg_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
@@ -77,7 +96,8 @@ def lib() -> ctypes.CDLL:
                    "tg_gated_attention", "tg_gated_attention_f16v", "tg_project_rope",
                    "tg_gated_attention_backward", "tg_gated_decode", "tg_debug_set_select_wait_limit", "tg_device_status",
                    "tg_project_rope_gather", "tg_topk_select_after_gate_kept_scores", "tg_topk_select_noalloc_status",
-                   "tg_debug_set_cta_pairs"):
+                   "tg_debug_set_cta_pairs", "tg_cache_append_q8", "tg_cache_read_q8", "tg_gated_decode_q8",
+                   "tg_cache_evict_q8"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -451,6 +471,148 @@ def tg_gated_decode(q, k_cache, v_cache, out, workspace, s_cache=None, gain=None
         Hq, Hkv, d_h, _ptr(s_cache), _ptr(gain), tau, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
         _stream(stream)))
     return out
+
+
+class CacheQ8:
+    """An 8-bit KV cache as the tg_cache_* calls and tg_gated_decode_q8 take it: the checked tensors and
+    the C struct that points to them.
+    k, v: [B, capacity, Hkv, d_h] torch.float8_e4m3fn or torch.int8 (heads dense in a token; K and V of equal
+    strides); k_scale, v_scale: [B, capacity / 32, Hkv] fp32; lengths: [B] int32; s, w: [B, capacity] fp32 or None."""
+
+    def __init__(self, k, v, k_scale, v_scale, lengths, s=None, w=None):
+        fmt = {torch.float8_e4m3fn: TG_CACHE_E4M3, torch.int8: TG_CACHE_INT8}.get(getattr(k, "dtype", None))
+        if fmt is None:
+            raise TypeError("k must be a torch.float8_e4m3fn or torch.int8 tensor")
+        _req(k, "k", k.dtype, 4)
+        _req(v, "v", k.dtype, 4)
+        B, cap, Hkv, d_h = k.shape
+        for t, n, dt, shape in ((k_scale, "k_scale", torch.float32, (B, cap // TG_CACHE_BLOCK, Hkv)),
+                                (v_scale, "v_scale", torch.float32, (B, cap // TG_CACHE_BLOCK, Hkv)),
+                                (lengths, "lengths", torch.int32, (B,)), (s, "s", torch.float32, (B, cap)),
+                                (w, "w", torch.float32, (B, cap))):
+            if t is None and n in ("s", "w"):
+                continue
+            _req(t, n, dt, len(shape))
+            if t is None or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous {list(shape)} tensor")
+        if v.shape != k.shape or cap % TG_CACHE_BLOCK:
+            raise ValueError("k and v must have one shape, the capacity a multiple of 32")
+        for t in (v, k_scale, v_scale, lengths, s, w):
+            if t is not None and t.device != k.device:
+                raise ValueError("a cache's tensors must be on one device")
+        ld_token, ld_seq = Hkv * d_h, cap * Hkv * d_h
+        if k.numel():
+            # strides of dimensions of one entry say nothing
+            strides = [tuple(st if n > 1 else None for st, n in zip(t.stride(), t.shape)) for t in (k, v)]
+            if strides[0] != strides[1] or strides[0][3] != 1 or strides[0][2] not in (None, d_h):
+                raise ValueError("k and v must have equal strides and heads dense in a token")
+            ld_token = strides[0][1] or ld_token
+            ld_seq = strides[0][0] or cap * ld_token
+        self.k, self.v, self.k_scale, self.v_scale, self.lengths, self.s, self.w = k, v, k_scale, v_scale, lengths, s, w
+        self.batch, self.capacity, self.Hkv, self.d_h, self.format, self.device = B, cap, Hkv, d_h, fmt, k.device
+        p = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
+        self.struct = CacheStruct(fmt, B, Hkv, d_h, cap, ld_token, ld_seq, p(k), p(v), p(k_scale), p(v_scale),
+                                  p(lengths), p(s), p(w))
+        self.ref = ctypes.byref(self.struct)
+
+    def on_device(self, *named):
+        for t, name in named:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} must be on the cache's device {self.device}")
+
+
+def _cache_call(cache, stream, call):
+    """`call(stream pointer)` with the cache's device current."""
+    if torch.cuda.current_device() == cache.device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(cache.device):
+        return call(_stream(stream))
+
+
+def tg_cache_workspace_bytes(cache: CacheQ8, n_q: int = 0, Hq: int = 0, accumulate: bool = False) -> int:
+    return int(lib().tg_cache_workspace_bytes(cache.ref, n_q, Hq, 1 if accumulate else 0))
+
+
+def tg_cache_append_q8(cache: CacheQ8, k, v, workspace, s_new=None, counts=None, stream=None):
+    """Appends k, v [B, n, Hkv, d_h] bf16 (heads dense; token and sequence strides free) as the last tokens of
+    every sequence: token i to slot lengths[b] - counts[b] + i (counts [B] int32; None: n each), so
+    cache.lengths hold the tokens after the append.  s_new: [B, n] fp32 biases."""
+    _req(k, "k", torch.bfloat16, 4)
+    _req(v, "v", torch.bfloat16, 4)
+    _req(s_new, "s_new", torch.float32, 2)
+    _req(counts, "counts", torch.int32, 1)
+    B, n = k.shape[:2]
+    if k.shape != v.shape or B != cache.batch or k.shape[2] != cache.Hkv or k.shape[3] != cache.d_h:
+        raise ValueError(f"k and v must be [{cache.batch}, n, {cache.Hkv}, {cache.d_h}]")
+    if s_new is not None and (tuple(s_new.shape) != (B, n) or not s_new.is_contiguous() or cache.s is None):
+        raise ValueError("s_new must be a contiguous [B, n] tensor, for a cache with s")
+    if counts is not None and (counts.shape[0] != B or not counts.is_contiguous()):
+        raise ValueError("counts must be a contiguous [B] tensor")
+    cache.on_device((k, "k"), (v, "v"), (s_new, "s_new"), (counts, "counts"), (workspace, "workspace"))
+    row = cache.Hkv * cache.d_h
+    lds = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t.numel() and (t.stride(3) != 1 or (cache.Hkv > 1 and t.stride(2) != cache.d_h)):
+            raise ValueError(f"{name}: heads must be dense in a token")
+        ld = t.stride(1) if n > 1 else row
+        lds.append((ld, t.stride(0) if B > 1 else ld * max(n, 1)))
+    _check("tg_cache_append_q8", _cache_call(cache, stream, lambda st: lib().tg_cache_append_q8(
+        cache.ref, _ptr(k), lds[0][0], lds[0][1], _ptr(v), lds[1][0], lds[1][1], n, _ptr(counts), _ptr(s_new),
+        _ptr(workspace), workspace.numel(), st)))
+    return cache
+
+
+def tg_cache_read_q8(cache: CacheQ8, k_out, v_out, first: int = 0, stream=None):
+    """Tokens [first, first + n) of every sequence as bf16 into k_out, v_out [B, n, Hkv, d_h] (contiguous);
+    rows at or beyond a sequence's length stay as they were."""
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _req(t, name, torch.bfloat16, 4)
+        if (t.shape[0], *t.shape[2:]) != (cache.batch, cache.Hkv, cache.d_h) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{cache.batch}, n, {cache.Hkv}, {cache.d_h}] tensor")
+    if k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have one shape")
+    cache.on_device((k_out, "k_out"), (v_out, "v_out"))
+    _check("tg_cache_read_q8", _cache_call(cache, stream, lambda st: lib().tg_cache_read_q8(
+        cache.ref, first, k_out.shape[1], _ptr(k_out), _ptr(v_out), st)))
+    return k_out, v_out
+
+
+def tg_gated_decode_q8(cache: CacheQ8, q, out, workspace, gain=None, tau: float = 1.0, accumulate: bool = False,
+                       max_len: int = 0, lse=None, stream=None):
+    """Decoding step over the cache: q [B, n_q, Hq, d_h] bf16, the queries of the last n_q tokens of every
+    sequence (query i sees the keys before lengths[b] - (n_q - 1 - i)); out like q; lse [B, n_q, Hq] fp32.
+    accumulate adds every key's softmax weight, over queries and heads, to cache.w.  max_len: an upper
+    bound on the lengths that sizes the launch (0: the capacity)."""
+    _req(q, "q", torch.bfloat16, 4)
+    _req(out, "out", torch.bfloat16, 4)
+    _req(gain, "gain", torch.float32, 1)
+    _req(lse, "lse", torch.float32, 3)
+    B, n_q, Hq, d_h = q.shape
+    if B != cache.batch or d_h != cache.d_h or out.shape != q.shape or not q.is_contiguous() or not out.is_contiguous():
+        raise ValueError(f"q and out must be contiguous [{cache.batch}, n_q, Hq, {cache.d_h}] tensors")
+    if gain is not None and (gain.shape[0] != Hq or not gain.is_contiguous()):
+        raise ValueError("gain must be a contiguous [Hq] tensor")
+    if lse is not None and (tuple(lse.shape) != (B, n_q, Hq) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [B, n_q, Hq] tensor")
+    cache.on_device((q, "q"), (out, "out"), (gain, "gain"), (lse, "lse"), (workspace, "workspace"))
+    _check("tg_gated_decode_q8", _cache_call(cache, stream, lambda st: lib().tg_gated_decode_q8(
+        cache.ref, _ptr(q), n_q, Hq, _ptr(gain), tau, 1 if accumulate else 0, max_len, _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel(), st)))
+    return out
+
+
+def tg_cache_evict_q8(src: CacheQ8, dst: CacheQ8, kept, workspace, budget: int, sink: int = 0, recent: int = 0,
+                      max_len: int = 0, stream=None):
+    """The first `sink`, the last `recent` and the heaviest (by src.w) other tokens of every sequence, `budget` in
+    all, into dst in ascending slot order; kept [B, budget] int32 gets their slots in src (-1 behind the last) and
+    dst.lengths their number."""
+    _req(kept, "kept", torch.int32, 2)
+    if tuple(kept.shape) != (src.batch, budget) or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous [B, budget] tensor")
+    src.on_device((dst.k, "dst"), (kept, "kept"), (workspace, "workspace"))
+    _check("tg_cache_evict_q8", _cache_call(src, stream, lambda st: lib().tg_cache_evict_q8(
+        src.ref, dst.ref, budget, sink, recent, max_len, _ptr(kept), _ptr(workspace), workspace.numel(), st)))
+    return kept
 
 
 def tg_debug_set_select_wait_limit(ns: int) -> None:
