@@ -7,29 +7,32 @@
 // The cache is read once: 2 d bytes a key and head, so HBM bounds a long step and latency a
 // short one.
 //
-// Work: a unit is one block (32 keys) of one head of one sequence.  The units of all
-// sequences, in order (sequence, head, block), are cut into equal runs, one for every thread block
-// of the launch (counted on the device from `lengths`, so one captured launch serves
-// growing and ragged sequences evenly); the warps of a thread block take the units of a run in
-// turn.  Each warp keeps its own running max, sum and output; they merge in shared memory when
-// a head's run ends, and a head that several thread blocks share is merged by the last of them to
-// arrive (a counter in the workspace), in the order of the runs, so results do not depend on timing.
+// Work: a unit is one block (32 keys) of one head of one sequence.  Short caches give every head a thread
+// block of its own.  Else the units of all sequences, in order (sequence, head, block), are cut
+// into equal runs, one for every SM (counted on the device from `lengths`, so one captured
+// launch serves growing and ragged sequences evenly); a run that crosses from one head to the next is
+// shared out among the warps in proportion, so that both heads are read at the same time.  Each warp
+// takes units of its head in turn and keeps its own reference, sum and output; the warps merge in shared memory, and
+// a second kernel merges the parts of heads that several thread blocks share, in the order of
+// the runs (no atomics: the same bits every time), and adds up the weights.
 //
-// A unit in a warp: K and V codes come straight from global memory into registers in the layout
-// of mma.m16n8k16's A operand -- keys (K) or head dimensions (V, transposed by byte
-// permutes) as the 16 rows, the query rows as the 8 columns of B: few queries waste
-// columns of a small MMA, not rows of a large one.  The order of d inside a dot product and of
-// the output's d over MMA rows is free, so every lane reads 16 contiguous bytes at a time and no
-// shared memory is involved.  S^T = K Q^T leaves weights whose 8x8 pieces movmatrix turns into the
-// B operand of O^T += V^T P^T.  Codes are exact in fp16.  The next unit's K is on its way
-// while this one's softmax and V product run, and the next V behind them.  (tcgen05 would take 128
-// keys a step from shared memory and bring the 8 columns back through TMEM; the products are far from
-// the bound here.)
+// A unit in a warp: codes come straight from global memory into registers in the layout of
+// mma.m16n8k16's A operand -- keys (K) or head dimensions (V, transposed by byte permutes) as the
+// 16 rows, the query rows as the 8 columns of B: few queries waste columns of a small MMA, not rows of a
+// large one.  The order of d inside a dot product and of the output's d over MMA rows is free, so every
+// lane reads 16 contiguous bytes at a time and no shared memory is involved.  S^T = K Q^T leaves
+// weights whose 8x8 pieces movmatrix turns into the B operand of O^T += V^T P^T.  Codes are exact in fp16.
+// The next unit's K is on its way while this one's V product runs, and the next V behind it.  (tcgen05 would
+// take 128 keys a step and bring the 8 columns back through TMEM; the products are far from the bound.)
+//
+// A row's reference m moves only when a logit exceeds it by more than 2^kLazy, and V's scales are folded into the
+// weights relative to a reference of their own, so the V product adds to the output in the MMA itself.
 //
 // Roundings: q is scaled to fp16 by a power of two per row (bf16 has fewer bits: only
-// elements 2^-25 of the row's largest are lost); the weights 2^(x - m + 15) are rounded to fp16 for
-// the V product (2^-12 each, below the output's bf16; the 15 keeps weights down to 2^-29 of the
-// largest normal), their sum is not.
+// elements 2^-25 of the row's largest are lost); the weights 2^(x - m + 8) vscale / vref are rounded to fp16
+// for the V product (2^-12 each, below the output's bf16; at most 2^15, and whole down to 2^-18 of the
+// reference weight, then in steps of 2^-28 of it, 2^16 times less than the bf16 output shows for any
+// 2^3 keys a unit of weight), their sum is not.
 #include <cmath>
 
 #include "tg_cache.cuh"
@@ -37,14 +40,20 @@
 namespace tg {
 namespace q8 {
 
-constexpr int kWarps = 4;
+// Warps of a thread block, one a SM: 168 registers a thread for up to 8 query rows, 255 for 16.
+constexpr int kDecWarps = 12;
+__host__ __device__ constexpr int warps_of(int NT) { return NT == 1 ? kDecWarps : 8; }
 constexpr int kMaxRows = 16;             // query rows per KV head
-constexpr int kMaxCtas = 148 * 8;
-constexpr int kMaxShare = 256;           // thread blocks that share one head at most (on average)
+constexpr int kMaxParts = 160;           // thread blocks of a launch that cuts the units into runs
+constexpr int kShortUnits = 2 * kDecWarps;   // heads up to this long get one thread block each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kShift = 15.0f;          // weights are 2^(x - m + kShift)
-constexpr int kWeightThreads = 256;
+constexpr float kShift = 8.0f;           // weights are 2^(x - m + kShift) ...
+constexpr float kLazy = 3.0f;            // ... at most 2^(kShift + kLazy) ...
+constexpr float kRatio = 16.0f;          // ... times vscale / vref, within 1 / kRatio .. kRatio
+constexpr float kNothing = -3.402823466e38f;   // the reference before the first logit
+constexpr int kFinThreads = 256, kWeightKeys = 64, kWeightGroups = kFinThreads / kWeightKeys;
+constexpr int kWeightTiles = kWeightGroups;   // tiles of keys at a time, one for each group to finish
 
 struct DecodeArgs {
     Cache c;
@@ -55,10 +64,12 @@ struct DecodeArgs {
     float scale_log2;                    // tau / sqrt(d) * log2(e)
     int n_q, Hq, G, R;
     int Rp;                              // R rounded up to even: a key's logits in the workspace
+    int short_heads;                     // one thread block a head
     unsigned int* status;
-    unsigned int* counter;               // [batch * Hkv], zero between calls
-    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units
-    float* part;                         // [2 * grid][R][2 + d]: m, l, o of a run's first / last head
+    int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
+    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
+    float* part;                         // [2 * grid][R][d]: sums of a run's first / last head
+    float2* part_ml;                     // [2 * grid][R]: their reference and sum
     float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
 };
 
@@ -98,19 +109,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// Sum over the block of one value per thread (every thread gets it).
-__device__ __forceinline__ long long block_sum(long long v, long long* s_warp) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
-    __syncthreads();
-    long long t = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) t += s_warp[w];
-    __syncthreads();
-    return t;
-}
-
 // The registers of one unit: per lane g = lane / 4, t = lane % 4, the K codes of keys 8 r + g
 // (r < 4), 16 bytes from 16 t of every 64; the V codes of keys 16 i + {2t, 2t + 1, 2t + 8, 2t + 9},
 // d / 8 bytes from g d / 8; scales and biases.
@@ -131,11 +129,17 @@ struct Warp {
     const int lane, g, t;
     uint32_t qf[D / 16][NT][2];
     float f[NT][2], gl2[NT][2];          // logit factor and gain of this lane's query rows 8 nt + 2 t + {0, 1}
-    int cut[NT][2];                      // keys those rows do not see at the sequence's end
-    float m[NT][2], l[NT][2], o[D / 16][NT][4];
+    float m[NT][2], l[NT][2], o[D / 16][NT][4];   // m: the reference less kShift
+    float vref;                          // o is in units of it
 
     __device__ __forceinline__ explicit Warp(const DecodeArgs& args)
         : a(args), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3) {}
+
+    // keys that the lane's row 8 nt + 2 t + c does not see at the sequence's end
+    __device__ __forceinline__ int cut(int nt, int c) const {
+        const int r = 8 * nt + 2 * t + c;
+        return r < a.R ? a.n_q - 1 - r / a.G : 0;
+    }
 
     // The query rows of one head: row r is query r / G, head kvh G + r % G.
     __device__ __forceinline__ void begin(int b, int kvh) {
@@ -173,9 +177,8 @@ struct Warp {
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // 2^e <= amax < 2^(e + 1): q 2^-e is below 2 (rows with infinities stay as they are)
             int e = (__float_as_int(amax) >> 23) - 127;
-            e = e > 127 ? 0 : max(e, -126);
-            const float down = __int_as_float((127 - min(e, 126)) << 23);
-            const float up = __fdiv_rn(1.0f, down);
+            e = e > 127 ? 0 : max(min(e, 126), -126);
+            const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 const float* y = &x[j / 4][4 * (j % 4)];
@@ -187,8 +190,7 @@ struct Warp {
                 f[nt][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + i)) * a.scale_log2;
                 const int rr = 8 * nt + 2 * t + i;
                 gl2[nt][i] = (rr < a.R && a.gain) ? __ldg(a.gain + kvh * a.G + rr % a.G) * kLog2e : 0.0f;
-                cut[nt][i] = rr < a.R ? a.n_q - 1 - rr / a.G : 0;
-                m[nt][i] = -INFINITY;
+                m[nt][i] = kNothing;
                 l[nt][i] = 0.0f;
             }
         }
@@ -198,36 +200,33 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[dm][nt][i] = 0.0f;
+        vref = 0.0f;
     }
 
-    __device__ __forceinline__ void load_keys(KeyRegs<D>& k, int b, int kvh, int blk) const {
-        const uint8_t* base = a.c.k + b * a.c.ld_seq + static_cast<int64_t>(blk) * kBlock * a.c.ld_token + kvh * D;
+    __device__ __forceinline__ void load_keys(KeyRegs<D>& k, const uint8_t* p, const float* scale, const float* s) const {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                load_codes<4>(base + (8 * r + g) * a.c.ld_token + 64 * i + 16 * t, &k.w[r][4 * i]);
-        k.scale = __ldg(a.c.k_scale + (b * a.c.blocks() + blk) * a.c.Hkv + kvh);
+            for (int i = 0; i < D / 64; ++i) load_codes<4>(p + 8 * r * a.c.ld_token + 64 * i, &k.w[r][4 * i]);
+        k.scale = __ldg(scale);
         if (a.c.s) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) k.s[r] = __ldg(a.c.s + b * a.c.capacity + blk * kBlock + 8 * r + g);
+            for (int r = 0; r < 4; ++r) k.s[r] = __ldg(s + 8 * r);
         }
     }
-    __device__ __forceinline__ void load_values(ValueRegs<D>& v, int b, int kvh, int blk) const {
-        const uint8_t* base = a.c.v + b * a.c.ld_seq + static_cast<int64_t>(blk) * kBlock * a.c.ld_token + kvh * D;
+    __device__ __forceinline__ void load_values(ValueRegs<D>& v, const uint8_t* p, const float* scale) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                load_codes<D / 32>(base + (16 * i + 2 * t + (j & 1) + 8 * (j >> 1)) * a.c.ld_token + g * (D / 8),
-                                   v.w[i][j]);
-        v.scale = __ldg(a.c.v_scale + (b * a.c.blocks() + blk) * a.c.Hkv + kvh);
+                load_codes<D / 32>(p + (16 * i + (j & 1) + 8 * (j >> 1)) * a.c.ld_token, v.w[i][j]);
+        v.scale = __ldg(scale);
     }
 
-    // Logits of a unit, the weights as B operands, the running max and sum; alpha: by how much
-    // the sums before shrink.
-    __device__ __forceinline__ void scores(const KeyRegs<D>& k, int b, int kvh, int blk, int len,
-                                           uint32_t (&pf)[2][NT][2], float (&alpha)[NT][2]) {
+    // Weights of a unit as B operands, times V's scale over its reference (fresh < 0) or for a product of
+    // its own that counts `fresh`; the sums.
+    __device__ __forceinline__ void scores(const KeyRegs<D>& k, float v_scale, int b, int kvh, int blk, int len,
+                                           uint32_t (&pf)[2][NT][2], float& fresh) {
         float x[2][NT][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -244,21 +243,34 @@ struct Warp {
             }
         }
         const bool bias = a.c.s && a.gain;
-        const bool ragged = (blk + 1) * kBlock > len - (a.n_q - 1);
+        if (bias) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float mx[2] = {-INFINITY, -INFINITY};
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float y = x[i][nt][c] * (f[nt][c & 1] * k.scale);
-                    if (bias) y = fmaf(gl2[nt][c & 1], k.s[2 * i + (c >> 1)], y);
-                    if (ragged && blk * kBlock + 16 * i + 8 * (c >> 1) + g >= len - cut[nt][c & 1]) y = -INFINITY;
-                    x[i][nt][c] = y;
-                    mx[c & 1] = fmaxf(mx[c & 1], y);
-                }
-            if constexpr (kWeights) {
+                    for (int c = 0; c < 4; ++c)
+                        x[i][nt][c] = fmaf(x[i][nt][c], f[nt][c & 1] * k.scale, gl2[nt][c & 1] * k.s[2 * i + (c >> 1)]);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[i][nt][c] *= f[nt][c & 1] * k.scale;
+        }
+        if ((blk + 1) * kBlock > len - (a.n_q - 1)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (blk * kBlock + 16 * i + 8 * (c >> 1) + g >= len - cut(nt, c & 1)) x[i][nt][c] = -INFINITY;
+        }
+        if constexpr (kWeights) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
                 if (8 * nt + 2 * t < a.R) {
                     float* to = a.logits +
                                 ((static_cast<int64_t>(b) * a.c.Hkv + kvh) * a.c.capacity + blk * kBlock + g) * a.Rp +
@@ -268,34 +280,84 @@ struct Warp {
                         *reinterpret_cast<float2*>(to + 8 * r * a.Rp) =
                             make_float2(x[r >> 1][nt][2 * (r & 1)], x[r >> 1][nt][2 * (r & 1) + 1]);
                 }
-            }
+        }
+        // the lane's own largest logits against the reference: it rarely has to move
+        bool move = false;
+        float mx[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
-                const float mn = fmaxf(m[nt][c], mx[c]);
-                const float base = mn == -INFINITY ? 0.0f : mn;      // nothing seen yet: every weight is 0
-                alpha[nt][c] = ex2(m[nt][c] - base);
-                m[nt][c] = mn;
-                l[nt][c] *= alpha[nt][c];
-                mx[c] = base - kShift;
+                mx[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+                move |= mx[nt][c] - m[nt][c] > kShift + kLazy;
             }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float top = mx[nt][c];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const float mn = fmaxf(m[nt][c], top - kShift);
+                    const float alpha = ex2(m[nt][c] - mn);
+                    m[nt][c] = mn;
+                    l[nt][c] *= alpha;
+#pragma unroll
+                    for (int dm = 0; dm < D / 16; ++dm) {
+                        o[dm][nt][c] *= alpha;
+                        o[dm][nt][c + 2] *= alpha;
+                    }
+                }
+        }
+        float ratio = __fdividef(v_scale, vref);
+        fresh = -1.0f;
+        if (!(ratio <= kRatio && ratio >= 1.0f / kRatio)) {
+            if (ratio < 1.0f / kRatio) {  // far smaller: a product of its own, added in fp32
+                fresh = ratio;
+            } else {                      // far larger, or the first: the new reference
+                const float shrink = __fdividef(vref, v_scale);
+#pragma unroll
+                for (int dm = 0; dm < D / 16; ++dm)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[dm][nt][c] *= shrink;
+                vref = v_scale;
+            }
+            ratio = 1.0f;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float p[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    p[c] = ex2(x[i][nt][c] - mx[c & 1]);
+                    p[c] = ex2(x[i][nt][c] - m[nt][c & 1]);
                     l[nt][c & 1] += p[c];
                 }
-                pf[i][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-                pf[i][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+                pf[i][nt][0] = transpose8x8(pack_f16x2(p[0] * ratio, p[1] * ratio));
+                pf[i][nt][1] = transpose8x8(pack_f16x2(p[2] * ratio, p[3] * ratio));
             }
-        }
     }
 
+    __device__ __forceinline__ void product(const ValueRegs<D>& v, int dm, const uint32_t (&pf)[2][NT][2],
+                                            float (&acc)[NT][4]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // bytes (key 2t, key 2t + 1) of head dimensions 2 dm and 2 dm + 1, and the same 8 keys on
+            const uint32_t sel = dm & 1 ? 0x7362 : 0x5140;
+            const uint32_t lo = __byte_perm(v.w[i][0][dm / 2], v.w[i][1][dm / 2], sel);
+            const uint32_t hi = __byte_perm(v.w[i][2][dm / 2], v.w[i][3][dm / 2], sel);
+            const uint32_t a0 = decode2<FMT, false>(lo), a1 = decode2<FMT, true>(lo);
+            const uint32_t a2 = decode2<FMT, false>(hi), a3 = decode2<FMT, true>(hi);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(acc[nt], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
+        }
+    }
     __device__ __forceinline__ void values(ValueRegs<D>& v, int blk, int len, const uint32_t (&pf)[2][NT][2],
-                                           const float (&alpha)[NT][2]) {
+                                           float fresh) {
         if ((blk + 1) * kBlock > len) {
             // rows behind the sequence may hold anything, NaN codes too: their weight is 0
 #pragma unroll
@@ -306,50 +368,49 @@ struct Warp {
 #pragma unroll
                         for (int w = 0; w < D / 32; ++w) v.w[i][j][w] = 0u;
         }
+        if (fresh < 0.0f) {
 #pragma unroll
-        for (int dm = 0; dm < D / 16; ++dm) {
-            float acc[NT][4];
+            for (int dm = 0; dm < D / 16; ++dm) product(v, dm, pf, o[dm]);
+        } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int dm = 0; dm < D / 16; ++dm) {
+                float acc[NT][4] = {};
+                product(v, dm, pf, acc);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[nt][c] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // bytes (key 2t, key 2t + 1) of head dimensions 2 dm and 2 dm + 1, and the same 8 keys on
-                const uint32_t sel = dm & 1 ? 0x7362 : 0x5140;
-                const uint32_t lo = __byte_perm(v.w[i][0][dm / 2], v.w[i][1][dm / 2], sel);
-                const uint32_t hi = __byte_perm(v.w[i][2][dm / 2], v.w[i][3][dm / 2], sel);
-                const uint32_t a0 = decode2<FMT, false>(lo), a1 = decode2<FMT, true>(lo);
-                const uint32_t a2 = decode2<FMT, false>(hi), a3 = decode2<FMT, true>(hi);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(acc[nt], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
+                    for (int c = 0; c < 4; ++c) o[dm][nt][c] = fmaf(fresh, acc[nt][c], o[dm][nt][c]);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    o[dm][nt][c] = fmaf(v.scale, acc[nt][c], o[dm][nt][c] * alpha[nt][c & 1]);
         }
     }
 
-    // Units u0 + warp, u0 + warp + kWarps, ... < u1 of one head.
-    __device__ __forceinline__ void run(int b, int kvh, int u0, int u1, int len) {
-        begin(b, kvh);
-        int u = u0 + (threadIdx.x >> 5);
+    // Units u0, u0 + step, ... < u1 of one head.
+    __device__ __forceinline__ void run(int b, int kvh, int u0, int u1, int step, int len) {
+        const int64_t block_codes = kBlock * a.c.ld_token, codes = b * a.c.ld_seq + u0 * block_codes + kvh * D;
+        const uint8_t* pk = a.c.k + codes + g * a.c.ld_token + 16 * t;
+        const uint8_t* pv = a.c.v + codes + 2 * t * a.c.ld_token + g * (D / 8);
+        const int64_t scale = (b * a.c.blocks() + u0) * a.c.Hkv + kvh;
+        const float *ks = a.c.k_scale + scale, *vs = a.c.v_scale + scale;
+        const float* s = a.c.s + b * a.c.capacity + u0 * kBlock + g;   // (used where there is an s)
         KeyRegs<D> k;
         ValueRegs<D> v;
-        if (u < u1) {
-            load_keys(k, b, kvh, u);
-            load_values(v, b, kvh, u);
+        if (u0 < u1) {
+            load_keys(k, pk, ks, s);
+            load_values(v, pv, vs);
         }
-        for (; u < u1; u += kWarps) {
+        begin(b, kvh);
+        for (int u = u0; u < u1; u += step) {
             uint32_t pf[2][NT][2];
-            float alpha[NT][2];
-            const int next = u + kWarps;
-            scores(k, b, kvh, u, len, pf, alpha);
-            if (next < u1) load_keys(k, b, kvh, next);
-            values(v, u, len, pf, alpha);
-            if (next < u1) load_values(v, b, kvh, next);
+            float fresh;
+            scores(k, v.scale, b, kvh, u, len, pf, fresh);
+            pk += step * block_codes;
+            pv += step * block_codes;
+            ks += step * a.c.Hkv;
+            vs += step * a.c.Hkv;
+            s += step * kBlock;
+            if (u + step < u1) load_keys(k, pk, ks, s);
+            values(v, u, len, pf, fresh);
+            if (u + step < u1) load_values(v, pv, vs);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -360,257 +421,434 @@ struct Warp {
     }
 };
 
-// One row's answer from its sums (weights carry 2^kShift).
-__device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int kvh, int r, float m, float l) {
-    const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l) - kShift;
-    a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + kvh) * kMaxRows + r] = lse2;
-    if (a.lse) a.lse[(static_cast<int64_t>(b) * a.n_q + r / a.G) * a.Hq + kvh * a.G + r % a.G] = lse2 * kLn2;
+__device__ __forceinline__ float row_lse2(float m, float l) { return l == 0.0f ? -INFINITY : m + log2f(l); }
+__device__ __forceinline__ int64_t out_row(const DecodeArgs& a, int b, int kvh, int r) {
+    return (static_cast<int64_t>(b) * a.n_q + r / a.G) * a.Hq + kvh * a.G + r % a.G;
 }
-__device__ __forceinline__ __nv_bfloat16* out_row(const DecodeArgs& a, int b, int kvh, int r, int D) {
-    return a.out + ((static_cast<int64_t>(b) * a.n_q + r / a.G) * a.Hq + kvh * a.G + r % a.G) * D;
+// Four outputs of one row: the sums over the warps or parts, divided by the row's sum.
+__device__ __forceinline__ void store_out(__nv_bfloat16* to, float4 o, float l) {
+    const float inv = __fdividef(1.0f, l);   // l < 2^11 * 2^31
+    uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (l == 0.0f) v = make_uint2(0u, 0u);   // no key, or none above -inf
+    *reinterpret_cast<uint2*>(to) = v;
+}
+__device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+}
+
+// A thread block's part of one head.
+struct Segment {
+    int b, kvh, len;
+    int u0, u1;                          // units of the head
+    int w0, w1;                          // the warps that take them
+    int parts;                           // thread blocks that share the head
+    int slot;                            // this thread block's part
+};
+
+template <int D, int NT>
+struct Shared {
+    static constexpr int kW = warps_of(NT);
+    float o[kW][8 * NT][D];       // the warps' sums
+    float m[kW][8 * NT], l[kW][8 * NT];
+    Segment seg[kW];
+    unsigned red[kW], base, next;
+    int n_seg, b;
+};
+
+// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace.
+template <int D, int FMT, int NT, bool kWeights>
+__device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& sh,
+                                            const Warp<D, FMT, NT, kWeights>& wp, int n_seg) {
+    constexpr int kThreads = warps_of(NT) * 32;
+    const int tid = threadIdx.x, warp = tid >> 5;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int r = 8 * nt + 2 * wp.t + c;
+            if (wp.g == 0) {
+                sh.m[warp][r] = wp.m[nt][c];
+                sh.l[warp][r] = wp.l[nt][c];
+            }
+            if (r < a.R) {
+                float* to = &sh.o[warp][r][D / 8 * wp.g];
+#pragma unroll
+                for (int dm = 0; dm < D / 16; ++dm)
+                    *reinterpret_cast<float2*>(to + 2 * dm) =
+                        make_float2(wp.o[dm][nt][c] * wp.vref, wp.o[dm][nt][2 + c] * wp.vref);
+            }
+        }
+    __syncthreads();
+    for (int i = tid; i < n_seg * a.R * (D / 4); i += kThreads) {
+        const int jr = i / (D / 4), j = jr / a.R, r = jr % a.R, d = i % (D / 4) * 4;
+        const Segment& sg = sh.seg[j];
+        float m = kNothing, l = 0.0f;
+        for (int w = sg.w0; w < sg.w1; ++w) m = fmaxf(m, sh.m[w][r]);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int w = sg.w0; w < sg.w1; ++w) {
+            const float f = ex2(sh.m[w][r] - m);
+            l = fmaf(sh.l[w][r], f, l);
+            add4(o, *reinterpret_cast<const float4*>(&sh.o[w][r][d]), f);
+        }
+        if (sg.parts == 1) {
+            store_out(a.out + out_row(a, sg.b, sg.kvh, r) * D + d, o, l);
+            if (d == 0) {
+                const float lse2 = row_lse2(m, l);
+                a.lse2[(static_cast<int64_t>(sg.b) * a.c.Hkv + sg.kvh) * kMaxRows + r] = lse2;
+                if (a.lse) a.lse[out_row(a, sg.b, sg.kvh, r)] = lse2 * kLn2;
+            }
+        } else {
+            *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(sg.slot) * a.R + r) * D + d) = o;
+            if (d == 0) a.part_ml[sg.slot * a.R + r] = make_float2(m, l);
+        }
+    }
 }
 
 template <int D, int FMT, int NT, bool kWeights>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2) gated_decode_q8_kernel(const DecodeArgs a) {
-    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
-    __shared__ __align__(16) float s_o[kWarps * 8 * NT * D];
-    __shared__ long long s_red[kWarps];
-    __shared__ int s_b;
-    __shared__ long long s_base;
-    __shared__ bool s_last;
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(const DecodeArgs a) {
+    constexpr int kW = warps_of(NT), kThreads = kW * 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_trigger();
     const int B = a.c.batch, Hkv = a.c.Hkv;
-    const int64_t G_all = gridDim.x;
+    Warp<D, FMT, NT, kWeights> wp(a);
 
-    // sequences without a token have no units: their rows are 0
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        if (length_of(a.c, b, a.status) > 0) continue;
-        for (int i = tid; i < a.n_q * a.Hq * D; i += kWarps * 32)
-            a.out[static_cast<int64_t>(b) * a.n_q * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
-        for (int i = tid; i < Hkv * a.R; i += kWarps * 32) finish_row(a, b, i / a.R, i % a.R, 0.0f, 0.0f);
+    if (a.short_heads) {
+        const int b = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv, len = length_of(a.c, b, a.status);
+        if (tid == 0) {
+            sh.seg[0] = Segment{b, kvh, len, 0, 0, 0, kW, 1, 0};
+            a.heads[blockIdx.x] = make_int2(0, 0);
+        }
+        wp.run(b, kvh, warp, (len + kBlock - 1) / kBlock, kW, len);
+        merge_warps<D, FMT, NT, kWeights>(a, sh, wp, 1);
+        return;
     }
 
-    // this thread block's run of units, and the sequence in which it begins
-    auto units_of = [&](int b) -> long long {
-        return static_cast<long long>((length_of(a.c, b, a.status) + kBlock - 1) / kBlock) * Hkv;
+    // All units (a unit is 4 KB of memory at least: their number fits 32 bits), this thread block's
+    // run of them and the sequence in which it begins; base: units before that sequence.
+    auto units_of = [&](int b) -> unsigned {
+        return static_cast<unsigned>((length_of(a.c, b, a.status) + kBlock - 1) / kBlock) * Hkv;
     };
-    long long total = 0;
+    auto scan = [&](unsigned mine, unsigned& before) -> unsigned {   // exclusive scan, returns the sum
+        unsigned incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.red[warp] = incl;
+        __syncthreads();
+        unsigned all = 0;
+        before = incl - mine;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            before += w < warp ? sh.red[w] : 0u;
+            all += sh.red[w];
+        }
+        __syncthreads();
+        return all;
+    };
+    unsigned total = 0, mine = 0, before = 0;
     if (B == 1) {
         total = units_of(0);
     } else {
-        for (int b = tid; b < B; b += kWarps * 32) total += units_of(b);
-        total = block_sum(total, s_red);
-    }
-    const long long n = G_all < total ? G_all : total;
-    if (blockIdx.x >= n) return;
-    long long u = total * blockIdx.x / n;
-    const long long u_end = total * (blockIdx.x + 1) / n;
-    const long long u_begin = u;
-    int b = 0;
-    long long base = 0;                   // units before sequence b
-    if (B > 1) {
-        for (int b0 = 0;; b0 += kWarps * 32) {
-            const long long mine = b0 + tid < B ? units_of(b0 + tid) : 0;
-            long long incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (lane == 31) s_red[warp] = incl;
-            __syncthreads();
-            long long before = base;
-            for (int w = 0; w < warp; ++w) before += s_red[w];
-            long long all = base;
-            for (int w = 0; w < kWarps; ++w) all += s_red[w];
-            if (before + incl - mine <= u && u < before + incl) {
-                s_b = b0 + tid;
-                s_base = before + incl - mine;
-            }
-            __syncthreads();
-            if (u < all) break;
-            base = all;
+        for (int b0 = 0; b0 < B; b0 += kThreads) {
+            mine = b0 + tid < B ? units_of(b0 + tid) : 0u;
+            total += scan(mine, before);
         }
-        b = s_b;
-        base = s_base;
     }
+    const unsigned n = gridDim.x < total ? gridDim.x : total;   // thread blocks with work
+    unsigned u = 0, u_end = 0;
+    if (blockIdx.x < n) {
+        u = static_cast<unsigned>(static_cast<uint64_t>(total) * blockIdx.x / n);
+        u_end = static_cast<unsigned>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / n);
+    }
+    const unsigned u_begin = u;
+    if (tid == 0) {
+        sh.b = 0;
+        sh.base = 0;
+    }
+    if (B > 1 && u < u_end) {
+        unsigned base = 0;
+        for (int b0 = 0;; b0 += kThreads) {
+            if (B > kThreads) {       // (a single round of sequences is still in registers)
+                mine = b0 + tid < B ? units_of(b0 + tid) : 0u;
+                const unsigned sum = scan(mine, before);
+                before += base;
+                base += sum;
+            } else {
+                __syncthreads();
+                base = total;
+            }
+            if (before <= u && u < before + mine) {
+                sh.b = b0 + tid;
+                sh.base = before;
+            }
+            if (u < base) break;
+        }
+    }
+    __syncthreads();
 
-    Warp<D, FMT, NT, kWeights> wp(a);
     while (u < u_end) {
-        const int len = length_of(a.c, b, a.status);
-        const int nblk = (len + kBlock - 1) / kBlock;
-        if (nblk == 0) {                  // nothing here: the next sequence
-            ++b;
-            continue;
-        }
-        const int kvh = static_cast<int>((u - base) / nblk);
-        const long long seg = base + static_cast<long long>(kvh) * nblk;
-        const long long stop = seg + nblk < u_end ? seg + nblk : u_end;
-        wp.run(b, kvh, static_cast<int>(u - seg), static_cast<int>(stop - seg), len);
-
-        // the warps' sums of this head
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (wp.g == 0) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    s_m[warp][8 * nt + 2 * wp.t + c] = wp.m[nt][c];
-                    s_l[warp][8 * nt + 2 * wp.t + c] = wp.l[nt][c];
+        // up to one head a warp: the next segments of the run
+        if (tid == 0) {
+            int k = 0, b = sh.b;
+            unsigned base = sh.base, v = u;
+            while (v < u_end && k < kW) {
+                const int len = length_of(a.c, b, a.status);
+                const unsigned nblk = (len + kBlock - 1) / kBlock;
+                if (nblk == 0) {         // nothing here: the next sequence
+                    ++b;
+                    continue;
+                }
+                const unsigned kvh = (v - base) / nblk, seg = base + kvh * nblk;
+                const unsigned stop = min(seg + nblk, u_end);
+                sh.seg[k] = Segment{b, static_cast<int>(kvh), len, static_cast<int>(v - seg), static_cast<int>(stop - seg),
+                                    0, 0, 1, static_cast<int>(2 * blockIdx.x + (seg < u_begin ? 0 : 1))};
+                ++k;
+                v = stop;
+                if (v == seg + nblk && kvh == static_cast<unsigned>(Hkv) - 1) {
+                    base += nblk * Hkv;
+                    ++b;
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int r = 8 * nt + 2 * wp.t + c;
-                if (r < a.R) {
-                    float* to = s_o + (warp * 8 * NT + r) * D + D / 8 * wp.g;
-#pragma unroll
-                    for (int dm = 0; dm < D / 16; ++dm)
-                        *reinterpret_cast<float2*>(to + 2 * dm) =
-                            make_float2(wp.o[dm][nt][c], wp.o[dm][nt][2 + c]);
+            sh.n_seg = k;
+            sh.b = b;
+            sh.base = base;
+            sh.next = v;
+        }
+        __syncthreads();
+        const int n_seg = sh.n_seg;
+        const unsigned u_next = sh.next, spare = kW - n_seg, units = u_next - u;
+        // every segment gets one warp, the others go by its units
+        unsigned seen = 0, my_seen = 0;
+        int my = 0, w0 = 0, w1 = kW;
+        if (n_seg > 1) {
+            for (int j = 0; j < n_seg; ++j) {
+                const int from = j + static_cast<int>(static_cast<uint64_t>(spare) * seen / units);
+                const unsigned c = sh.seg[j].u1 - sh.seg[j].u0;
+                const int to = j + 1 + static_cast<int>(static_cast<uint64_t>(spare) * (seen + c) / units);
+                if (warp >= from && warp < to) {
+                    my = j;
+                    w0 = from;
+                    w1 = to;
+                    my_seen = seen;
                 }
+                seen += c;
+            }
+        }
+        Segment& sg = sh.seg[my];
+        if (lane == 0 && warp == w0) {
+            // the thread blocks holding the head's first and last unit
+            const unsigned nblk = (sg.len + kBlock - 1) / kBlock, seg = u + my_seen - sg.u0;
+            const int i0 = static_cast<int>(((seg + 1ull) * n - 1) / total);
+            const int i1 = static_cast<int>((static_cast<uint64_t>(seg + nblk) * n - 1) / total);
+            sg.w0 = w0;
+            sg.w1 = w1;
+            sg.parts = i1 - i0 + 1;
+            if (sg.u0 == 0) a.heads[sg.b * Hkv + sg.kvh] = make_int2(i0, i0 == i1 ? 0 : i1 - i0 + 1);
+        }
+        wp.run(sg.b, sg.kvh, sg.u0 + warp - w0, sg.u1, w1 - w0, sg.len);
+        merge_warps<D, FMT, NT, kWeights>(a, sh, wp, n_seg);
+        __syncthreads();
+        u = u_next;
+    }
+
+    // sequences without a token have no units: their rows are 0
+    for (int e = blockIdx.x; e < B; e += gridDim.x) {
+        if (length_of(a.c, e, a.status) > 0) continue;
+        for (int i = tid; i < a.n_q * a.Hq * D; i += kThreads)
+            a.out[static_cast<int64_t>(e) * a.n_q * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
+        for (int i = tid; i < a.n_q * a.Hq; i += kThreads)
+            if (a.lse) a.lse[static_cast<int64_t>(e) * a.n_q * a.Hq + i] = -INFINITY;
+        for (int i = tid; i < Hkv; i += kThreads) a.heads[e * Hkv + i] = make_int2(0, 0);
+    }
+}
+
+// The second kernel: thread block (x, b).  With weights, every thread block first gathers the log-sum-exps of all
+// rows of its sequence (from the parts' references and sums, or those that are done); block x merges the heads
+// x, x + gridDim.x, ... that have parts, and adds the weights of keys x * 64, ...: w[b, c] += sum over heads and
+// rows of 2^(x - lse2), 4 tiles of 64 keys and 4 groups of heads at a time so that many loads are under way at once,
+// the groups' sums in a fixed order.  About two thread blocks a SM: the log-sum-exps cost each as much as some tiles.
+template <int D>
+__global__ void __launch_bounds__(kFinThreads) decode_q8_finish_kernel(const DecodeArgs a, int weights) {
+    __shared__ float s_lse[64 * kMaxRows];
+    __shared__ float s_f[kMaxParts][kMaxRows], s_l[kMaxRows];
+    __shared__ float4 s_sum[kFinThreads];
+    const int tid = threadIdx.x, b = blockIdx.y, Hkv = a.c.Hkv;
+    pdl_wait();
+    pdl_trigger();
+    // part p of a head belongs to thread block i0 + p: its last head for p = 0, its first one otherwise
+    auto slot = [](int i0, int p) -> int64_t { return 2 * (i0 + p) + (p == 0); };
+    if (weights) {
+        // 8 lanes a row
+        for (int i = tid / 8; i < (Hkv * a.Rp + 3) / 4 * 4; i += kFinThreads / 8) {
+            const int h = i / a.Rp, r = i % a.Rp;
+            float m = kNothing, l = 0.0f;
+            const bool row = h < Hkv && r < a.R;
+            const int2 hd = row ? a.heads[b * Hkv + h] : make_int2(0, 0);
+            for (int p = tid % 8; p < hd.y; p += 8) {
+                const float2 x = __ldcg(a.part_ml + slot(hd.x, p) * a.R + r);
+                const float mn = fmaxf(m, x.x);
+                l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
+                m = mn;
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+                const float mn = fmaxf(m, m2);
+                l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
+                m = mn;
+            }
+            if (tid % 8 == 0 && h < Hkv) {
+                float v = hd.y ? row_lse2(m, l) : -INFINITY;
+                if (row && hd.y == 0 && length_of(a.c, b, a.status) > 0)
+                    v = a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r];
+                s_lse[i] = v == -INFINITY ? INFINITY : v;   // a row that saw nothing adds nothing
             }
         }
         __syncthreads();
-        // thread blocks that share this head: those holding its first and last unit, and all between
-        const long long i0 = ((seg + 1) * n - 1) / total, i1 = ((seg + nblk) * n - 1) / total;
-        const bool whole = i0 == i1;
-        float* part = a.part + (2 * blockIdx.x + (seg < u_begin ? 0 : 1)) * static_cast<int64_t>(a.R) * (2 + D);
-        for (int i = tid; i < a.R * D; i += kWarps * 32) {
-            const int r = i / D, d = i % D;
-            float mx = -INFINITY;
+    }
+    for (int h = blockIdx.x; h < Hkv; h += gridDim.x) {
+        const int2 hd = a.heads[b * Hkv + h];
+        const int np = hd.y;
+        if (np == 0) continue;
+        // groups of threads take the parts in turn; the first of them are under way while the factors form
+        const int vecs = a.R * (D / 4), groups = vecs >= kFinThreads ? 1 : kFinThreads / vecs;
+        const int grp = groups > 1 ? tid / vecs : 0;
+        for (int i0 = 0; i0 < vecs; i0 += kFinThreads) {
+            const int i = groups > 1 ? tid % vecs : i0 + tid;
+            const bool active = groups > 1 ? grp < groups : i < vecs;
+            constexpr int kAhead = 10;
+            float4 x[kAhead];
+            const float* from = a.part + static_cast<int64_t>(active ? i : 0) * 4;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
-            const float ref = mx == -INFINITY ? 0.0f : mx;
-            float ls = 0.0f, os = 0.0f;
+            for (int y = 0; y < kAhead; ++y)
+                if (active && grp + y * groups < np)
+                    x[y] = __ldcg(reinterpret_cast<const float4*>(from + slot(hd.x, grp + y * groups) * a.R * D));
+            if (i0 == 0) {
+                for (int r = tid / 32; r < a.R; r += kFinThreads / 32) {
+                    constexpr int kPer = kMaxParts / 32;
+                    float2 ml[kPer];
+                    float m = kNothing, l = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float fw = ex2(s_m[w][r] - ref);
-                ls += s_l[w][r] * fw;
-                os += s_o[(w * 8 * NT + r) * D + d] * fw;
-            }
-            if (whole) {
-                out_row(a, b, kvh, r, D)[d] = __float2bfloat16_rn(ls == 0.0f ? 0.0f : os / ls);
-                if (d == 0) finish_row(a, b, kvh, r, ref, ls);
-            } else {
-                part[r * (2 + D) + 2 + d] = os;
-                if (d == 0) {
-                    part[r * (2 + D)] = mx;
-                    part[r * (2 + D) + 1] = ls;
-                }
-            }
-        }
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            unsigned int* count = a.counter + static_cast<int64_t>(b) * Hkv + kvh;
-            if (tid == 0) s_last = atomicAdd(count, 1u) == static_cast<unsigned>(i1 - i0);
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const int np = static_cast<int>(i1 - i0) + 1;
-                // part p belongs to thread block i0 + p: its last head for p = 0, its first one otherwise
-                const float* parts = a.part;
-                const int64_t ld = static_cast<int64_t>(a.R) * (2 + D);
-                for (int i = tid; i < a.R * D; i += kWarps * 32) {
-                    const int r = i / D, d = i % D;
-                    float mx = -INFINITY;
-                    for (int p = 0; p < np; ++p)
-                        mx = fmaxf(mx, __ldcg(parts + (2 * (i0 + p) + (p == 0)) * ld + r * (2 + D)));
-                    const float ref = mx == -INFINITY ? 0.0f : mx;
-                    float ls = 0.0f, os = 0.0f;
-                    for (int p = 0; p < np; ++p) {
-                        const float* pr = parts + (2 * (i0 + p) + (p == 0)) * ld + r * (2 + D);
-                        const float fp = ex2(__ldcg(pr) - ref);
-                        ls += __ldcg(pr + 1) * fp;
-                        os += __ldcg(pr + 2 + d) * fp;
+                    for (int y = 0; y < kPer; ++y) {
+                        const int p = tid % 32 + 32 * y;
+                        ml[y] = p < np ? __ldcg(a.part_ml + slot(hd.x, p) * a.R + r) : make_float2(kNothing, 0.0f);
+                        m = fmaxf(m, ml[y].x);
                     }
-                    out_row(a, b, kvh, r, D)[d] = __float2bfloat16_rn(ls == 0.0f ? 0.0f : os / ls);
-                    if (d == 0) finish_row(a, b, kvh, r, ref, ls);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+                    for (int y = 0; y < kPer; ++y) {
+                        const float f = ex2(ml[y].x - m);
+                        l = fmaf(ml[y].y, f, l);
+                        if (tid % 32 + 32 * y < np) s_f[tid % 32 + 32 * y][r] = f;
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    if (tid % 32 == 0) {
+                        s_l[r] = l;
+                        if (a.lse) a.lse[out_row(a, b, h, r)] = row_lse2(m, l) * kLn2;
+                    }
                 }
-                if (tid == 0) *count = 0u;   // ready for the next call
+                __syncthreads();
+            }
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (active) {
+#pragma unroll
+                for (int y = 0; y < kAhead; ++y)
+                    if (grp + y * groups < np) add4(o, x[y], s_f[grp + y * groups][r]);
+#pragma unroll 8
+                for (int p = grp + kAhead * groups; p < np; p += groups)
+                    add4(o, __ldcg(reinterpret_cast<const float4*>(from + slot(hd.x, p) * a.R * D)), s_f[p][r]);
+            }
+            if (groups > 1) {
+                if (active) s_sum[tid] = o;
+                __syncthreads();
+                if (tid < vecs) {
+                    for (int y = 1; y < groups; ++y) add4(o, s_sum[y * vecs + tid], 1.0f);
+                    store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
+                }
+            } else if (active) {
+                store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
             }
         }
-        __syncthreads();                  // the shared sums are free again
-        u = stop;
-        if (u == seg + nblk && kvh == Hkv - 1) {
-            base += static_cast<long long>(nblk) * Hkv;
-            ++b;
+        __syncthreads();                  // the next head uses the same room
+    }
+    if (!weights) return;
+    const int len = length_of(a.c, b, a.status), key = tid % kWeightKeys, grp = tid / kWeightKeys;
+    const int pairs = a.Rp / 2, items = Hkv * pairs;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWeightKeys;
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWeightKeys; c0 < len; c0 += kWeightTiles * stride) {
+        float sum[kWeightTiles] = {};
+        const float* x = a.logits + (static_cast<int64_t>(b) * Hkv * a.c.capacity + c0 + key) * a.Rp;
+#pragma unroll 2
+        for (int i = grp; i < items; i += kWeightGroups) {
+            const int h = i / pairs, r = 2 * (i % pairs);
+            const float l0 = s_lse[h * a.Rp + r], l1 = s_lse[h * a.Rp + r + 1];
+#pragma unroll
+            for (int j = 0; j < kWeightTiles; ++j)
+                if (c0 + key + j * stride < len) {
+                    const float2 y = __ldcg(
+                        reinterpret_cast<const float2*>(x + (h * a.c.capacity + j * stride) * a.Rp + r));
+                    sum[j] += ex2(y.x - l0);
+                    if (r + 1 < a.R) sum[j] += ex2(y.y - l1);
+                }
         }
+        float* sums = reinterpret_cast<float*>(s_sum);   // [tile][group][key]
+#pragma unroll
+        for (int j = 0; j < kWeightTiles; ++j) sums[j * kFinThreads + tid] = sum[j];
+        __syncthreads();
+        // one group a tile
+        const int64_t c = c0 + key + grp * stride;
+        if (c < len) {
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWeightGroups; ++i) total += sums[grp * kFinThreads + i * kWeightKeys + key];
+            a.c.w[b * a.c.capacity + c] += total;
+        }
+        __syncthreads();
     }
 }
 
-// w[b, c] += sum over the heads' rows of 2^(x - lse2): one thread a key, a fixed order.
-__global__ void __launch_bounds__(kWeightThreads) decode_q8_weights_kernel(const DecodeArgs a) {
-    __shared__ float s_lse[64 * kMaxRows];
-    pdl_wait();
-    pdl_trigger();
-    const int b = blockIdx.y, len = length_of(a.c, b, a.status);
-    for (int i = threadIdx.x; i < a.c.Hkv * a.Rp; i += kWeightThreads) {
-        const int h = i / a.Rp, r = i % a.Rp;
-        const float v = r < a.R ? a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + h) * kMaxRows + r] : INFINITY;
-        s_lse[i] = v == -INFINITY ? INFINITY : v;   // a row that saw nothing adds nothing
-    }
-    __syncthreads();
-    for (int64_t c = static_cast<int64_t>(blockIdx.x) * kWeightThreads + threadIdx.x; c < len;
-         c += static_cast<int64_t>(gridDim.x) * kWeightThreads) {
-        float sum = 0.0f;
-        for (int h = 0; h < a.c.Hkv; ++h) {
-            const float* x = a.logits + ((static_cast<int64_t>(b) * a.c.Hkv + h) * a.c.capacity + c) * a.Rp;
-            for (int r = 0; r < a.Rp; r += 2) {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(x + r));
-                sum += ex2(y.x - s_lse[h * a.Rp + r]);
-                if (r + 1 < a.R) sum += ex2(y.y - s_lse[h * a.Rp + r + 1]);
-            }
-        }
-        a.c.w[b * a.c.capacity + c] += sum;
-    }
-}
-
-// Workspace: status header, counters, lse2, parts, logits (each from a 256-byte boundary).
+// Workspace: status header, heads, lse2, parts, logits (each from a 256-byte boundary).
 struct Layout {
-    size_t counter, lse2, part, logits, bytes;
+    size_t heads, lse2, part, part_ml, logits, bytes;
 };
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-static int max_grid(int64_t heads) {
-    return static_cast<int>(heads * kMaxShare < kMaxCtas ? heads * kMaxShare : kMaxCtas);
-}
 static Layout layout(const Cache& c, int d_h, int R, bool weights) {
     const int64_t heads = static_cast<int64_t>(c.batch) * c.Hkv;
     Layout L;
-    L.counter = kWsHeader;
-    L.lse2 = L.counter + up256(static_cast<size_t>(heads) * 4);
+    L.heads = kWsHeader;
+    L.lse2 = L.heads + up256(static_cast<size_t>(heads) * 8);
     L.part = L.lse2 + up256(static_cast<size_t>(heads) * kMaxRows * 4);
-    L.logits = L.part + up256(static_cast<size_t>(max_grid(heads)) * 2 * R * (2 + d_h) * 4);
+    L.part_ml = L.part + up256(static_cast<size_t>(2 * kMaxParts) * R * d_h * 4);
+    L.logits = L.part_ml + up256(static_cast<size_t>(2 * kMaxParts) * R * 8);
     L.bytes = L.logits + (weights ? up256(static_cast<size_t>(heads) * c.capacity * ((R + 1) / 2 * 2) * 4) : 0);
     return L;
 }
 
 template <int D, int FMT, int NT, bool kWeights>
-static tg_status launch(const DecodeArgs& a, int64_t max_units, cudaStream_t st) {
-    static std::atomic<int> occ_cache[64];
-    const int dev = current_device();
+static tg_status launch(const DecodeArgs& a, int grid, cudaStream_t st) {
+    static std::atomic<int> smem_set[64];
     auto kern = gated_decode_q8_kernel<D, FMT, NT, kWeights>;
-    int occ = dev >= 0 ? occ_cache[dev].load(std::memory_order_relaxed) : 0;
-    if (occ <= 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kWarps * 32, 0) != cudaSuccess || occ <= 0) occ = 1;
-        if (dev >= 0) occ_cache[dev].store(occ, std::memory_order_relaxed);
-    }
-    // one wave of resident thread blocks, a unit for every warp
-    int64_t grid = static_cast<int64_t>(num_sms()) * occ;
-    const int64_t most = max_grid(static_cast<int64_t>(a.c.batch) * a.c.Hkv);
-    if (grid > most) grid = most;
-    if (grid > (max_units + kWarps - 1) / kWarps) grid = (max_units + kWarps - 1) / kWarps;
-    if (grid < 1) grid = 1;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0, st, a);
+    constexpr int kSmem = static_cast<int>(sizeof(Shared<D, NT>));
+    if (!set_max_dynamic_smem(kern, kSmem, smem_set)) return TG_ERR_CUDA;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(warps_of(NT) * 32), kSmem, st, a);
 }
 
 template <int D, int FMT>
-static tg_status launch_rows(const DecodeArgs& a, bool weights, int64_t max_units, cudaStream_t st) {
-    if (a.R <= 8)
-        return weights ? launch<D, FMT, 1, true>(a, max_units, st) : launch<D, FMT, 1, false>(a, max_units, st);
-    return weights ? launch<D, FMT, 2, true>(a, max_units, st) : launch<D, FMT, 2, false>(a, max_units, st);
+static tg_status launch_rows(const DecodeArgs& a, bool weights, int grid, cudaStream_t st) {
+    if (a.R <= 8) return weights ? launch<D, FMT, 1, true>(a, grid, st) : launch<D, FMT, 1, false>(a, grid, st);
+    return weights ? launch<D, FMT, 2, true>(a, grid, st) : launch<D, FMT, 2, false>(a, grid, st);
 }
 
 }  // namespace q8
@@ -658,25 +896,31 @@ extern "C" tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16*
     a.n_q = n_q;
     a.Hq = Hq;
     a.status = status_word(workspace);
-    a.counter = reinterpret_cast<unsigned int*>(ws + L.counter);
+    a.heads = reinterpret_cast<int2*>(ws + L.heads);
     a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
     a.part = reinterpret_cast<float*>(ws + L.part);
+    a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
     a.logits = reinterpret_cast<float*>(ws + L.logits);
     if (max_len == 0 || max_len > a.c.capacity) max_len = a.c.capacity;
-    const int64_t max_units = (max_len + q8::kBlock - 1) / q8::kBlock * a.c.Hkv * a.c.batch;
+    // one thread block a head where every warp has at most two units of it, else one a SM
+    const int64_t heads = static_cast<int64_t>(a.c.batch) * a.c.Hkv, blocks = (max_len + q8::kBlock - 1) / q8::kBlock;
+    a.short_heads = blocks <= q8::kShortUnits;
+    const int sms = num_sms() < q8::kMaxParts ? num_sms() : q8::kMaxParts;
+    const int grid = static_cast<int>(a.short_heads ? heads : sms);
     cudaStream_t st = as_stream(stream);
     const bool w = accumulate != 0 && a.c.capacity > 0;
     tg_status r;
     if (cache->d_h == 128)
-        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<128, TG_CACHE_E4M3>(a, w, max_units, st)
-                                           : q8::launch_rows<128, TG_CACHE_INT8>(a, w, max_units, st);
+        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<128, TG_CACHE_E4M3>(a, w, grid, st)
+                                           : q8::launch_rows<128, TG_CACHE_INT8>(a, w, grid, st);
     else
-        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, max_units, st)
-                                           : q8::launch_rows<64, TG_CACHE_INT8>(a, w, max_units, st);
-    if (r != TG_OK || !w) return r;
-    int64_t blocks = (max_len + q8::kWeightThreads - 1) / q8::kWeightThreads;
-    if (blocks > 4096) blocks = 4096;
-    return q8::launch_pdl(q8::decode_q8_weights_kernel,
-                          dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks), static_cast<unsigned>(a.c.batch)),
-                          dim3(q8::kWeightThreads), 0, st, a);
+        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, grid, st)
+                                           : q8::launch_rows<64, TG_CACHE_INT8>(a, w, grid, st);
+    if (r != TG_OK || (a.short_heads && !w)) return r;
+    int64_t x = w ? (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys : 1;
+    if (x > 2 * sms / a.c.batch) x = 2 * sms / a.c.batch;   // (the rest by the kernel's stride)
+    if (!a.short_heads && x < a.c.Hkv) x = a.c.Hkv;
+    const dim3 fin(static_cast<unsigned>(x < 1 ? 1 : x), static_cast<unsigned>(a.c.batch));
+    return q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>, fin,
+                          dim3(q8::kFinThreads), 0, st, a, static_cast<int>(w));
 }
