@@ -84,11 +84,12 @@ class KVCacheQ8:
                tau: float = 1.0, lse: Optional[torch.Tensor] = None, accumulate: bool = False,
                max_len: int = 0) -> torch.Tensor:
         """tg_gated_decode_q8: attention of the last n_q tokens' queries q [B, n_q, Hq, d_h] over the cache."""
-        if q.dim() != 4:
+        shape = q.shape
+        if len(shape) != 4:
             raise ValueError("q must be [B, n_q, Hq, d_h]")
-        ws = self.reserve(q.shape[1], q.shape[2], accumulate)
-        return tg.tg_gated_decode_q8(self.handle, q, torch.empty_like(q) if out is None else out, ws, gain=gain,
-                                     tau=tau, accumulate=accumulate, max_len=max_len, lse=lse)
+        ws = self.reserve(shape[1], shape[2], accumulate)
+        return tg.tg_gated_decode_q8(self.handle, q, torch.empty_like(q) if out is None else out, ws, gain, tau,
+                                     accumulate, max_len, lse)
 
     def read(self, k_out: torch.Tensor, v_out: torch.Tensor, first: int = 0):
         """tg_cache_read_q8: tokens from `first` on as bf16 into k_out, v_out [B, n, Hkv, d_h]."""

@@ -213,14 +213,16 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadAr
 // ------------------------------------------------------------------------------------------- evict
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kCluster = 8;              // thread blocks that select for one sequence
+constexpr int kCluster = 8;              // thread blocks that select for one long sequence
+constexpr int kMostKeys = 48 * 1024;     // keys a thread block holds in shared memory
+constexpr int kOneBlockKeys = 16 * 1024; // sequences up to this long are selected by one thread block
 
 struct EvictArgs {
     Cache src, dst;
     int64_t budget, sink, recent;
     int32_t* kept;
     unsigned int* status;
-    int cached;                          // keys of a thread block that fit its shared memory
+    int cached;                          // keys of a thread block that its shared memory has room for
 };
 
 __device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t rank) {
@@ -230,49 +232,49 @@ __device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t rank) {
 }
 
 // Exclusive scan over the block of one value per thread; *total is the block's sum.
-__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* s_warp, unsigned* total) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned incl = v;
+    T incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+        const T y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        unsigned w = s_warp[lane];
+    // every warp adds up the warps before it
+    T w = s_warp[lane];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        s_warp[lane] = w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    __syncthreads();
-    const unsigned before = (warp ? s_warp[warp - 1] : 0u) + incl - v;
-    *total = s_warp[kSelWarps - 1];
-    __syncthreads();
-    return before;
+    *total = __shfl_sync(0xffffffffu, w, kSelWarps - 1);
+    const T before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    return (warp ? before : 0) + incl - v;
 }
 
-// One cluster per sequence: kept[b, :] ascending, dst's length.  Each thread block owns a contiguous
-// eighth of the tokens between the sinks and the recent ones (keys in shared memory where they fit, else read again
-// from L2 each pass), each warp a contiguous part of that.
-__global__ void __launch_bounds__(kSelThreads, 1) __cluster_dims__(kCluster, 1, 1)
-cache_evict_select_kernel(const EvictArgs a) {
+// CL thread blocks per sequence (one, or a cluster): kept[b, :] ascending, dst's length.  Each thread block owns a
+// contiguous part of the tokens between the sinks and the recent ones (their keys in shared memory where they fit,
+// else read again from L2 each pass), each warp a contiguous part of that.  A sequence is a few KB to a few 100 KB:
+// what bounds the select is the latency of its steps, so a short sequence does without a cluster's barriers.
+template <int CL>
+__global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(const EvictArgs a) {
     extern __shared__ uint32_t s_key[];
     __shared__ unsigned s_hist[3][2048];  // one a pass, so that a peer may still read the last one
-    __shared__ unsigned s_warp[kSelWarps];
-    __shared__ unsigned s_pick[2], s_cnt[2], s_before[2];
+    __shared__ unsigned s_scan[4][kSelWarps];
+    __shared__ unsigned long long s_scan2[kSelWarps];
+    __shared__ unsigned s_pick[3][2], s_cnt[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_rank_in();
+    const uint32_t rank = CL > 1 ? cluster_rank_in() : 0;
+    for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.y;
     const int n = length_of(a.src, b, a.status);
     int32_t* kept = a.kept + b * a.budget;
-    const int gtid = rank * kSelThreads + tid, gthreads = kCluster * kSelThreads;
+    const int gtid = rank * kSelThreads + tid, gthreads = CL * kSelThreads;
     if (gtid == 0) a.dst.lengths[b] = static_cast<int32_t>(n < a.budget ? n : a.budget);
     if (n <= a.budget) {                 // the whole cluster: nothing leaves
         for (int64_t i = gtid; i < a.budget; i += gthreads) kept[i] = i < n ? static_cast<int32_t>(i) : -1;
@@ -286,104 +288,111 @@ cache_evict_select_kernel(const EvictArgs a) {
 
     // this block's span [c0, c1) and this warp's part of it
     const int m = n - sink - recent;
-    const int per = (m + kCluster - 1) / kCluster;
+    const int per = (m + CL - 1) / CL;
     const int c0 = min(static_cast<int>(rank) * per, m), c1 = min(c0 + per, m), cn = c1 - c0;
     const int wper = ((per + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
     const int w0 = min(warp * wper, cn), w1 = min(w0 + wper, cn);
     const float* w = a.src.w + b * a.src.capacity + sink + c0;
     const bool cached = per <= a.cached;
     auto key_at = [&](int i) { return cached ? s_key[i] : radix_key(__ldcg(w + i)); };
+    auto count = [&](unsigned* hist, bool match, uint32_t digit) {
+        // one count where a warp's keys agree (ties), else one each
+        const unsigned active = __ballot_sync(0xffffffffu, match);
+        if (match) {
+            int same;
+            __match_all_sync(active, digit, &same);
+            if (!same)
+                atomicAdd(&hist[digit], 1u);
+            else if (lane == __ffs(active) - 1)
+                atomicAdd(&hist[digit], static_cast<unsigned>(__popc(active)));
+        }
+    };
+    __syncthreads();                     // the histograms are zero
 
     uint32_t prefix = 0, pmask = 0;
     unsigned krem = static_cast<unsigned>(kd);   // rank of the threshold among the keys that match `prefix`
-    for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
-    __syncthreads();
 #pragma unroll 1
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : (p == 1 ? 10 : 0), nb = p == 2 ? 1024 : 2048;
-        for (int i0 = 0; i0 < cn; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            uint32_t key = 0;
-            if (i < cn) {
-                if (p == 0) {
-                    key = radix_key(__ldcg(w + i));
-                    if (cached) s_key[i] = key;
-                } else {
-                    key = key_at(i);
-                }
+        for (int i0 = 0; i0 < cn; i0 += 8 * kSelThreads) {
+            uint32_t key[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * kSelThreads + tid;
+                key[j] = 0u;
+                if (i < cn) key[j] = p == 0 ? radix_key(__ldcg(w + i)) : key_at(i);
             }
-            const bool match = i < cn && (key & pmask) == prefix;
-            const unsigned active = __ballot_sync(0xffffffffu, match);
-            if (match) {
-                const uint32_t digit = (key >> shift) & (nb - 1);
-                const unsigned peers = __match_any_sync(active, digit);
-                if (lane == __ffs(peers) - 1) atomicAdd(&s_hist[p][digit], static_cast<unsigned>(__popc(peers)));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * kSelThreads + tid;
+                if (i0 + j * kSelThreads >= cn) break;
+                if (p == 0 && cached && i < cn) s_key[i] = key[j];
+                count(s_hist[p], i < cn && (key[j] & pmask) == prefix, (key[j] >> shift) & (nb - 1));
             }
         }
-        cluster_sync_all();
+        if (CL > 1) cluster_sync_all();
+        else __syncthreads();
         // every thread block sums the whole histogram: two bins a thread, from the top digit down
         unsigned c[2] = {0u, 0u};
         const int d0 = nb - 1 - 2 * tid;
         if (d0 > 0) {
-            uint32_t x[2][kCluster];
+            if constexpr (CL == 1) {
+                c[0] = s_hist[p][d0];
+                c[1] = s_hist[p][d0 - 1];
+            } else {
+                uint32_t x[2][CL];
 #pragma unroll
-            for (int r = 0; r < kCluster; ++r) {
-                x[0][r] = cluster_ld(&s_hist[p][d0], r);
-                x[1][r] = cluster_ld(&s_hist[p][d0 - 1], r);
-            }
+                for (int r = 0; r < CL; ++r) {
+                    x[0][r] = cluster_ld(&s_hist[p][d0], r);
+                    x[1][r] = cluster_ld(&s_hist[p][d0 - 1], r);
+                }
 #pragma unroll
-            for (int r = 0; r < kCluster; ++r) {
-                c[0] += x[0][r];
-                c[1] += x[1][r];
+                for (int r = 0; r < CL; ++r) {
+                    c[0] += x[0][r];
+                    c[1] += x[1][r];
+                }
             }
         }
         unsigned tot;
-        const unsigned e = block_scan(c[0] + c[1], s_warp, &tot);
+        const unsigned e = block_scan(c[0] + c[1], s_scan[p], &tot);
         if (e < krem && krem <= e + c[0]) {
-            s_pick[0] = d0;
-            s_pick[1] = e;
+            s_pick[p][0] = d0;
+            s_pick[p][1] = e;
         } else if (e + c[0] < krem && krem <= e + c[0] + c[1]) {
-            s_pick[0] = d0 - 1;
-            s_pick[1] = e + c[0];
+            s_pick[p][0] = d0 - 1;
+            s_pick[p][1] = e + c[0];
         }
         __syncthreads();
-        prefix |= s_pick[0] << shift;
+        prefix |= s_pick[p][0] << shift;
         pmask |= static_cast<uint32_t>(nb - 1) << shift;
-        krem -= s_pick[1];
-        __syncthreads();
+        krem -= s_pick[p][1];
     }
     // keys above the threshold `prefix` stay, and the first krem equal to it
     unsigned gt = 0, eq = 0;
     for (int i0 = w0; i0 < w1; i0 += 32) {
-        const uint32_t key = i0 + lane < w1 ? key_at(i0 + lane) : 0u;
         const bool in = i0 + lane < w1;
+        const uint32_t key = in ? key_at(i0 + lane) : 0u;
         gt += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
         eq += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
     }
-    unsigned gt_all, eq_all;
-    unsigned gt_before = block_scan(lane == 0 ? gt : 0u, s_warp, &gt_all);
-    unsigned eq_before = block_scan(lane == 0 ? eq : 0u, s_warp, &eq_all);
-    if (tid == 0) {
-        s_cnt[0] = gt_all;
-        s_cnt[1] = eq_all;
-    }
-    cluster_sync_all();
-    if (warp == 0) {
-        unsigned x = 0, y = 0;
+    unsigned long long all;
+    unsigned long long mine = block_scan(lane == 0 ? static_cast<unsigned long long>(gt) << 32 | eq : 0ull, s_scan2, &all);
+    if (CL > 1) {
+        if (tid == 0) {
+            s_cnt[0] = static_cast<unsigned>(all >> 32);
+            s_cnt[1] = static_cast<unsigned>(all);
+        }
+        cluster_sync_all();
+        unsigned x = 0, y = 0;           // every warp: the counts of the blocks before this one
         if (lane < static_cast<int>(rank)) {
             x = cluster_ld(&s_cnt[0], lane);
             y = cluster_ld(&s_cnt[1], lane);
         }
-        x = __reduce_add_sync(0xffffffffu, x);
-        y = __reduce_add_sync(0xffffffffu, y);
-        if (lane == 0) {
-            s_before[0] = x;
-            s_before[1] = y;
-        }
+        mine += static_cast<unsigned long long>(__reduce_add_sync(0xffffffffu, x)) << 32 |
+                __reduce_add_sync(0xffffffffu, y);
     }
-    __syncthreads();
-    gt_before = __shfl_sync(0xffffffffu, gt_before, 0) + s_before[0];
-    eq_before = __shfl_sync(0xffffffffu, eq_before, 0) + s_before[1];
+    mine = __shfl_sync(0xffffffffu, mine, 0);
+    unsigned gt_before = static_cast<unsigned>(mine >> 32), eq_before = static_cast<unsigned>(mine);
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const bool in = i0 + lane < w1;
         const uint32_t key = in ? key_at(i0 + lane) : 0u;
@@ -396,12 +405,12 @@ cache_evict_select_kernel(const EvictArgs a) {
         gt_before += __popc(mg);
         eq_before += __popc(me);
     }
-    cluster_sync_all();                  // no block leaves while a peer may read its shared memory
+    if (CL > 1) cluster_sync_all();      // no block leaves while a peer may read its shared memory
 }
 
 // One warp: one new block of one head, K or V.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) cache_evict_gather_kernel(const EvictArgs a) {
     constexpr int LPR = D / 16;          // lanes of a row of codes
     constexpr int RPL = 32 / LPR;
     constexpr int N = kBlock / RPL;
@@ -417,12 +426,10 @@ __global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const E
     const float* from_scale = (is_v ? a.src.v_scale : a.src.k_scale) + b * a.src.blocks() * Hkv + head;
     const float mine = slot >= 0 ? __ldg(from_scale + static_cast<int64_t>(slot / kBlock) * Hkv) : 0.0f;
     uint4 u[N];
-    float sc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int r = i * RPL + lane / LPR;
         const int at = __shfl_sync(0xffffffffu, slot, r);
-        sc[i] = __shfl_sync(0xffffffffu, mine, r);
         u[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(from + at * a.src.ld_token)) : make_uint4(0u, 0u, 0u, 0u);
     }
     float amax = 0.0f;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const E
             decode4<FMT>(top, f);
         else
             f[0] = static_cast<float>(top);
-        amax = fmaxf(amax, f[0] * sc[i]);
+        amax = fmaxf(amax, f[0] * __shfl_sync(0xffffffffu, mine, i * RPL + lane / LPR));
     }
     const float scale = scale_for<FMT>(warp_max(amax));
     uint8_t* to = (is_v ? a.dst.v : a.dst.k) + b * a.dst.ld_seq + j * kBlock * a.dst.ld_token + head * D +
@@ -459,8 +466,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const E
         const int r = i * RPL + lane / LPR;
         const int at = __shfl_sync(0xffffffffu, slot, r);
         uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        if (sc[i] != scale) {
-            const float ratio = __fdiv_rn(sc[i], scale);
+        const float before = __shfl_sync(0xffffffffu, mine, r);
+        if (before != scale) {
+            const float ratio = __fdiv_rn(before, scale);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 float f[4];
@@ -476,6 +484,29 @@ __global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const E
         if (a.dst.s && a.src.s) a.dst.s[at] = a.src.s[of];
         if (a.dst.w) a.dst.w[at] = a.src.w[of];
     }
+}
+
+template <int CL>
+static tg_status launch_select(EvictArgs a, int64_t max_len, cudaStream_t st) {
+    static std::atomic<int> smem_set[64];
+    auto kern = cache_evict_select_kernel<CL>;
+    constexpr int kMost = (CL == 1 ? kOneBlockKeys : kMostKeys) * 4;
+    if (!set_max_dynamic_smem(kern, kMost, smem_set)) return TG_ERR_CUDA;
+    const int64_t per = (max_len + CL - 1) / CL;
+    a.cached = per * 4 <= kMost ? static_cast<int>(per) : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CL, static_cast<unsigned>(a.src.batch));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.cached) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2] = {pdl_attr()};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CL;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? launch_status() : TG_ERR_CUDA;
 }
 
 // Whether [p, p + bytes) and [q, q + more) share memory.
@@ -588,15 +619,12 @@ extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8
     a.kept = kept;
     a.status = status_word(workspace);
     if (max_len == 0 || max_len > src->capacity) max_len = src->capacity;
-    // keys of a thread block in its shared memory (beside 25 KB of histograms) where they fit
-    constexpr int kMostCached = 48 * 1024;
-    int64_t per = (max_len + q8::kCluster - 1) / q8::kCluster;
-    a.cached = per <= kMostCached ? static_cast<int>(per) : 0;
-    static std::atomic<int> smem_set[64];
-    if (!set_max_dynamic_smem(q8::cache_evict_select_kernel, kMostCached * 4, smem_set)) return TG_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    tg_status r = q8::launch_pdl(q8::cache_evict_select_kernel, dim3(q8::kCluster, static_cast<unsigned>(src->batch)),
-                                 dim3(q8::kSelThreads), static_cast<size_t>(a.cached) * 4, st, a);
+    tg_status r;
+    if (max_len <= q8::kOneBlockKeys)
+        r = q8::launch_select<1>(a, max_len, st);
+    else
+        r = q8::launch_select<q8::kCluster>(a, max_len, st);
     if (r != TG_OK || budget == 0) return r;
     const int64_t units = (budget + q8::kBlock - 1) / q8::kBlock * src->Hkv * 2;
     const dim3 grid(static_cast<unsigned>((units + q8::kWarps - 1) / q8::kWarps), static_cast<unsigned>(src->batch));

@@ -14,7 +14,7 @@
 // shared out among the warps in proportion, so that both heads are read at the same time.  Each warp
 // takes units of its head in turn and keeps its own reference, sum and output; the warps merge in shared memory, and
 // a second kernel merges the parts of heads that several thread blocks share, in the order of
-// the runs (no atomics: the same bits every time), and adds up the weights.
+// the runs (no atomics: the same bits every time); a third adds up the weights where they are gathered.
 //
 // A unit in a warp: codes come straight from global memory into registers in the layout of
 // mma.m16n8k16's A operand -- keys (K) or head dimensions (V, transposed by byte permutes) as the
@@ -67,7 +67,7 @@ struct DecodeArgs {
     int short_heads;                     // one thread block a head
     unsigned int* status;
     int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
-    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
+    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units
     float* part;                         // [2 * grid][R][d]: sums of a run's first / last head
     float2* part_ml;                     // [2 * grid][R]: their reference and sum
     float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
@@ -668,123 +668,106 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
         for (int i = tid; i < a.n_q * a.Hq; i += kThreads)
             if (a.lse) a.lse[static_cast<int64_t>(e) * a.n_q * a.Hq + i] = -INFINITY;
         for (int i = tid; i < Hkv; i += kThreads) a.heads[e * Hkv + i] = make_int2(0, 0);
+        for (int i = tid; i < Hkv * kMaxRows; i += kThreads)
+            a.lse2[static_cast<int64_t>(e) * Hkv * kMaxRows + i] = -INFINITY;
     }
 }
 
-// The second kernel: thread block (x, b).  With weights, every thread block first gathers the log-sum-exps of all
-// rows of its sequence (from the parts' references and sums, or those that are done); block x merges the heads
-// x, x + gridDim.x, ... that have parts, and adds the weights of keys x * 64, ...: w[b, c] += sum over heads and
-// rows of 2^(x - lse2), 4 tiles of 64 keys and 4 groups of heads at a time so that many loads are under way at once,
-// the groups' sums in a fixed order.  About two thread blocks a SM: the log-sum-exps cost each as much as some tiles.
+// Merges the parts of heads that several thread blocks share: thread block (h, b), in the order of the parts.
 template <int D>
-__global__ void __launch_bounds__(kFinThreads) decode_q8_finish_kernel(const DecodeArgs a, int weights) {
-    __shared__ float s_lse[64 * kMaxRows];
+__global__ void __launch_bounds__(kFinThreads) decode_q8_finish_kernel(const DecodeArgs a) {
     __shared__ float s_f[kMaxParts][kMaxRows], s_l[kMaxRows];
     __shared__ float4 s_sum[kFinThreads];
-    const int tid = threadIdx.x, b = blockIdx.y, Hkv = a.c.Hkv;
+    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
     pdl_wait();
     pdl_trigger();
-    // part p of a head belongs to thread block i0 + p: its last head for p = 0, its first one otherwise
-    auto slot = [](int i0, int p) -> int64_t { return 2 * (i0 + p) + (p == 0); };
-    if (weights) {
-        // 8 lanes a row
-        for (int i = tid / 8; i < (Hkv * a.Rp + 3) / 4 * 4; i += kFinThreads / 8) {
-            const int h = i / a.Rp, r = i % a.Rp;
-            float m = kNothing, l = 0.0f;
-            const bool row = h < Hkv && r < a.R;
-            const int2 hd = row ? a.heads[b * Hkv + h] : make_int2(0, 0);
-            for (int p = tid % 8; p < hd.y; p += 8) {
-                const float2 x = __ldcg(a.part_ml + slot(hd.x, p) * a.R + r);
-                const float mn = fmaxf(m, x.x);
-                l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
-                m = mn;
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-                const float mn = fmaxf(m, m2);
-                l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
-                m = mn;
-            }
-            if (tid % 8 == 0 && h < Hkv) {
-                float v = hd.y ? row_lse2(m, l) : -INFINITY;
-                if (row && hd.y == 0 && length_of(a.c, b, a.status) > 0)
-                    v = a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r];
-                s_lse[i] = v == -INFINITY ? INFINITY : v;   // a row that saw nothing adds nothing
-            }
-        }
-        __syncthreads();
-    }
-    for (int h = blockIdx.x; h < Hkv; h += gridDim.x) {
-        const int2 hd = a.heads[b * Hkv + h];
-        const int np = hd.y;
-        if (np == 0) continue;
-        // groups of threads take the parts in turn; the first of them are under way while the factors form
-        const int vecs = a.R * (D / 4), groups = vecs >= kFinThreads ? 1 : kFinThreads / vecs;
-        const int grp = groups > 1 ? tid / vecs : 0;
-        for (int i0 = 0; i0 < vecs; i0 += kFinThreads) {
-            const int i = groups > 1 ? tid % vecs : i0 + tid;
-            const bool active = groups > 1 ? grp < groups : i < vecs;
-            constexpr int kAhead = 10;
-            float4 x[kAhead];
-            const float* from = a.part + static_cast<int64_t>(active ? i : 0) * 4;
-#pragma unroll
-            for (int y = 0; y < kAhead; ++y)
-                if (active && grp + y * groups < np)
-                    x[y] = __ldcg(reinterpret_cast<const float4*>(from + slot(hd.x, grp + y * groups) * a.R * D));
-            if (i0 == 0) {
-                for (int r = tid / 32; r < a.R; r += kFinThreads / 32) {
-                    constexpr int kPer = kMaxParts / 32;
-                    float2 ml[kPer];
-                    float m = kNothing, l = 0.0f;
-#pragma unroll
-                    for (int y = 0; y < kPer; ++y) {
-                        const int p = tid % 32 + 32 * y;
-                        ml[y] = p < np ? __ldcg(a.part_ml + slot(hd.x, p) * a.R + r) : make_float2(kNothing, 0.0f);
-                        m = fmaxf(m, ml[y].x);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
-                    for (int y = 0; y < kPer; ++y) {
-                        const float f = ex2(ml[y].x - m);
-                        l = fmaf(ml[y].y, f, l);
-                        if (tid % 32 + 32 * y < np) s_f[tid % 32 + 32 * y][r] = f;
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    if (tid % 32 == 0) {
-                        s_l[r] = l;
-                        if (a.lse) a.lse[out_row(a, b, h, r)] = row_lse2(m, l) * kLn2;
-                    }
-                }
-                __syncthreads();
-            }
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (active) {
-#pragma unroll
+    // part p of a head belongs to thread block hd.x + p: its last head for p = 0, its first one otherwise
+    const int2 hd = a.heads[b * a.c.Hkv + h];
+    auto slot = [&](int p) -> int64_t { return 2 * (hd.x + p) + (p == 0); };
+    const int np = hd.y;
+    if (np == 0) return;
+            // groups of threads take the parts in turn; the first of them are under way while the factors form
+            const int vecs = a.R * (D / 4), groups = vecs >= kFinThreads ? 1 : kFinThreads / vecs;
+            const int grp = groups > 1 ? tid / vecs : 0;
+            for (int i0 = 0; i0 < vecs; i0 += kFinThreads) {
+                const int i = groups > 1 ? tid % vecs : i0 + tid;
+                const bool active = groups > 1 ? grp < groups : i < vecs;
+                constexpr int kAhead = 10;
+                float4 x[kAhead];
+                const float* from = a.part + static_cast<int64_t>(active ? i : 0) * 4;
+    #pragma unroll
                 for (int y = 0; y < kAhead; ++y)
-                    if (grp + y * groups < np) add4(o, x[y], s_f[grp + y * groups][r]);
-#pragma unroll 8
-                for (int p = grp + kAhead * groups; p < np; p += groups)
-                    add4(o, __ldcg(reinterpret_cast<const float4*>(from + slot(hd.x, p) * a.R * D)), s_f[p][r]);
-            }
-            if (groups > 1) {
-                if (active) s_sum[tid] = o;
-                __syncthreads();
-                if (tid < vecs) {
-                    for (int y = 1; y < groups; ++y) add4(o, s_sum[y * vecs + tid], 1.0f);
+                    if (active && grp + y * groups < np)
+                        x[y] = __ldcg(reinterpret_cast<const float4*>(from + slot(grp + y * groups) * a.R * D));
+                if (i0 == 0) {
+                    for (int r = tid / 32; r < a.R; r += kFinThreads / 32) {
+                        constexpr int kPer = kMaxParts / 32;
+                        float2 ml[kPer];
+                        float m = kNothing, l = 0.0f;
+    #pragma unroll
+                        for (int y = 0; y < kPer; ++y) {
+                            const int p = tid % 32 + 32 * y;
+                            ml[y] = p < np ? __ldcg(a.part_ml + slot(p) * a.R + r) : make_float2(kNothing, 0.0f);
+                            m = fmaxf(m, ml[y].x);
+                        }
+    #pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    #pragma unroll
+                        for (int y = 0; y < kPer; ++y) {
+                            const float f = ex2(ml[y].x - m);
+                            l = fmaf(ml[y].y, f, l);
+                            if (tid % 32 + 32 * y < np) s_f[tid % 32 + 32 * y][r] = f;
+                        }
+    #pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                        if (tid % 32 == 0) {
+                            s_l[r] = l;
+                            const float lse2 = row_lse2(m, l);
+                        a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + h) * kMaxRows + r] = lse2;
+                        if (a.lse) a.lse[out_row(a, b, h, r)] = lse2 * kLn2;
+                        }
+                    }
+                    __syncthreads();
+                }
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (active) {
+    #pragma unroll
+                    for (int y = 0; y < kAhead; ++y)
+                        if (grp + y * groups < np) add4(o, x[y], s_f[grp + y * groups][r]);
+    #pragma unroll 8
+                    for (int p = grp + kAhead * groups; p < np; p += groups)
+                        add4(o, __ldcg(reinterpret_cast<const float4*>(from + slot(p) * a.R * D)), s_f[p][r]);
+                }
+                if (groups > 1) {
+                    if (active) s_sum[tid] = o;
+                    __syncthreads();
+                    if (tid < vecs) {
+                        for (int y = 1; y < groups; ++y) add4(o, s_sum[y * vecs + tid], 1.0f);
+                        store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
+                    }
+                } else if (active) {
                     store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
                 }
-            } else if (active) {
-                store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
             }
-        }
-        __syncthreads();                  // the next head uses the same room
+}
+
+// w[b, c] += sum over heads and rows of 2^(x - lse2): 64 keys and 4 groups of heads a thread block, up to 4 tiles of
+// keys at once so that many loads are under way, the groups' sums in a fixed order.
+__global__ void __launch_bounds__(kFinThreads) decode_q8_weights_kernel(const DecodeArgs a) {
+    __shared__ float s_lse[64 * kMaxRows];
+    __shared__ float s_sum[kWeightTiles][kWeightGroups][kWeightKeys];
+    const int tid = threadIdx.x, b = blockIdx.y, Hkv = a.c.Hkv, key = tid % kWeightKeys, grp = tid / kWeightKeys;
+    pdl_wait();
+    pdl_trigger();
+    const int len = length_of(a.c, b, a.status);
+    if (static_cast<int64_t>(blockIdx.x) * kWeightKeys >= len) return;
+    for (int i = tid; i < Hkv * a.Rp; i += kFinThreads) {
+        const int h = i / a.Rp, r = i % a.Rp;
+        const float v = r < a.R ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : INFINITY;
+        s_lse[i] = v == -INFINITY ? INFINITY : v;   // a row that saw nothing adds nothing
     }
-    if (!weights) return;
-    const int len = length_of(a.c, b, a.status), key = tid % kWeightKeys, grp = tid / kWeightKeys;
+    __syncthreads();
     const int pairs = a.Rp / 2, items = Hkv * pairs;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWeightKeys;
     for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWeightKeys; c0 < len; c0 += kWeightTiles * stride) {
@@ -792,27 +775,25 @@ __global__ void __launch_bounds__(kFinThreads) decode_q8_finish_kernel(const Dec
         const float* x = a.logits + (static_cast<int64_t>(b) * Hkv * a.c.capacity + c0 + key) * a.Rp;
 #pragma unroll 2
         for (int i = grp; i < items; i += kWeightGroups) {
-            const int h = i / pairs, r = 2 * (i % pairs);
+            const int h = i / pairs, r = 2 * (i - h * pairs);
             const float l0 = s_lse[h * a.Rp + r], l1 = s_lse[h * a.Rp + r + 1];
 #pragma unroll
             for (int j = 0; j < kWeightTiles; ++j)
                 if (c0 + key + j * stride < len) {
-                    const float2 y = __ldcg(
-                        reinterpret_cast<const float2*>(x + (h * a.c.capacity + j * stride) * a.Rp + r));
+                    const float2 y =
+                        __ldcg(reinterpret_cast<const float2*>(x + (h * a.c.capacity + j * stride) * a.Rp + r));
                     sum[j] += ex2(y.x - l0);
                     if (r + 1 < a.R) sum[j] += ex2(y.y - l1);
                 }
         }
-        float* sums = reinterpret_cast<float*>(s_sum);   // [tile][group][key]
 #pragma unroll
-        for (int j = 0; j < kWeightTiles; ++j) sums[j * kFinThreads + tid] = sum[j];
+        for (int j = 0; j < kWeightTiles; ++j) s_sum[j][grp][key] = sum[j];
         __syncthreads();
-        // one group a tile
-        const int64_t c = c0 + key + grp * stride;
+        const int64_t c = c0 + key + grp * stride;   // one group a tile
         if (c < len) {
             float total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWeightGroups; ++i) total += sums[grp * kFinThreads + i * kWeightKeys + key];
+            for (int i = 0; i < kWeightGroups; ++i) total += s_sum[grp][i][key];
             a.c.w[b * a.c.capacity + c] += total;
         }
         __syncthreads();
@@ -916,11 +897,14 @@ extern "C" tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16*
     else
         r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, grid, st)
                                            : q8::launch_rows<64, TG_CACHE_INT8>(a, w, grid, st);
-    if (r != TG_OK || (a.short_heads && !w)) return r;
-    int64_t x = w ? (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys : 1;
-    if (x > 2 * sms / a.c.batch) x = 2 * sms / a.c.batch;   // (the rest by the kernel's stride)
-    if (!a.short_heads && x < a.c.Hkv) x = a.c.Hkv;
-    const dim3 fin(static_cast<unsigned>(x < 1 ? 1 : x), static_cast<unsigned>(a.c.batch));
-    return q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>, fin,
-                          dim3(q8::kFinThreads), 0, st, a, static_cast<int>(w));
+    const dim3 per_head(static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.c.batch));
+    if (r == TG_OK && !a.short_heads)
+        r = q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>,
+                           per_head, dim3(q8::kFinThreads), 0, st, a);
+    if (r != TG_OK || !w) return r;
+    int64_t x = (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys;
+    if (x > 8 * sms / a.c.batch) x = 8 * sms / a.c.batch;   // (the rest by the kernel's stride)
+    return q8::launch_pdl(q8::decode_q8_weights_kernel,
+                          dim3(static_cast<unsigned>(x < 1 ? 1 : x), static_cast<unsigned>(a.c.batch)),
+                          dim3(q8::kFinThreads), 0, st, a);
 }

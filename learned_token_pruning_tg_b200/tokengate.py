@@ -510,23 +510,42 @@ class CacheQ8:
             ld_seq = strides[0][0] or cap * ld_token
         self.k, self.v, self.k_scale, self.v_scale, self.lengths, self.s, self.w = k, v, k_scale, v_scale, lengths, s, w
         self.batch, self.capacity, self.Hkv, self.d_h, self.format, self.device = B, cap, Hkv, d_h, fmt, k.device
+        self.index = k.get_device()
         p = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
         self.struct = CacheStruct(fmt, B, Hkv, d_h, cap, ld_token, ld_seq, p(k), p(v), p(k_scale), p(v_scale),
                                   p(lengths), p(s), p(w))
         self.ref = ctypes.byref(self.struct)
 
-    def on_device(self, *named):
-        for t, name in named:
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name} must be on the cache's device {self.device}")
+    def check(self, t, name, dtype, shape):
+        """t: a contiguous tensor of this type and shape on the cache's device (a decoding step makes a few
+        calls a layer, so each check reads as little of a tensor as it can)."""
+        if t.dtype is dtype and t.get_device() == self.index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+        _req(t, name, dtype, len(shape))
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on the cache's device {self.device}")
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
 
 
-def _cache_call(cache, stream, call):
-    """`call(stream pointer)` with the cache's device current."""
-    if torch.cuda.current_device() == cache.device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(cache.device):
-        return call(_stream(stream))
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _cache_call(name, fn, cache, stream, *args):
+    """fn(*args, stream pointer) with the cache's device current."""
+    if torch.cuda.current_device() == cache.index:
+        status = fn(*args, _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(cache.index):
+            status = fn(*args, _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    if status != TG_OK:
+        raise TokenGateError(name, status)
+
+
+def _cache_workspace(cache, workspace):
+    if workspace.get_device() != cache.index:
+        raise ValueError(f"workspace must be on the cache's device {cache.device}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def tg_cache_workspace_bytes(cache: CacheQ8, n_q: int = 0, Hq: int = 0, accumulate: bool = False) -> int:
@@ -537,43 +556,37 @@ def tg_cache_append_q8(cache: CacheQ8, k, v, workspace, s_new=None, counts=None,
     """Appends k, v [B, n, Hkv, d_h] bf16 (heads dense; token and sequence strides free) as the last tokens of
     every sequence: token i to slot lengths[b] - counts[b] + i (counts [B] int32; None: n each), so
     cache.lengths hold the tokens after the append.  s_new: [B, n] fp32 biases."""
-    _req(k, "k", torch.bfloat16, 4)
-    _req(v, "v", torch.bfloat16, 4)
-    _req(s_new, "s_new", torch.float32, 2)
-    _req(counts, "counts", torch.int32, 1)
-    B, n = k.shape[:2]
-    if k.shape != v.shape or B != cache.batch or k.shape[2] != cache.Hkv or k.shape[3] != cache.d_h:
-        raise ValueError(f"k and v must be [{cache.batch}, n, {cache.Hkv}, {cache.d_h}]")
-    if s_new is not None and (tuple(s_new.shape) != (B, n) or not s_new.is_contiguous() or cache.s is None):
-        raise ValueError("s_new must be a contiguous [B, n] tensor, for a cache with s")
-    if counts is not None and (counts.shape[0] != B or not counts.is_contiguous()):
-        raise ValueError("counts must be a contiguous [B] tensor")
-    cache.on_device((k, "k"), (v, "v"), (s_new, "s_new"), (counts, "counts"), (workspace, "workspace"))
-    row = cache.Hkv * cache.d_h
+    B, Hkv, d_h = cache.batch, cache.Hkv, cache.d_h
+    row = Hkv * d_h
+    n = k.shape[1] if k.dim() == 4 else 0
     lds = []
     for t, name in ((k, "k"), (v, "v")):
-        if t.numel() and (t.stride(3) != 1 or (cache.Hkv > 1 and t.stride(2) != cache.d_h)):
+        if t.dtype is not torch.bfloat16 or t.get_device() != cache.index or t.shape != (B, n, Hkv, d_h):
+            _req(t, name, torch.bfloat16, 4)
+            if t.get_device() != cache.index:
+                raise ValueError(f"{name} must be on the cache's device {cache.device}")
+            raise ValueError(f"k and v must be [{B}, n, {Hkv}, {d_h}]")
+        sb, st, sh, sd = t.stride()
+        if (sd != 1 or (sh != d_h and Hkv > 1)) and t.numel():
             raise ValueError(f"{name}: heads must be dense in a token")
-        ld = t.stride(1) if n > 1 else row
-        lds.append((ld, t.stride(0) if B > 1 else ld * max(n, 1)))
-    _check("tg_cache_append_q8", _cache_call(cache, stream, lambda st: lib().tg_cache_append_q8(
-        cache.ref, _ptr(k), lds[0][0], lds[0][1], _ptr(v), lds[1][0], lds[1][1], n, _ptr(counts), _ptr(s_new),
-        _ptr(workspace), workspace.numel(), st)))
+        ld = st if n > 1 else row
+        lds.append((t.data_ptr(), ld, sb if B > 1 else ld * max(n, 1)))
+    if s_new is not None and cache.s is None:
+        raise ValueError("s_new is for a cache with s")
+    ws, ws_bytes = _cache_workspace(cache, workspace)
+    _cache_call("tg_cache_append_q8", lib().tg_cache_append_q8, cache, stream, cache.ref, *lds[0], *lds[1], n,
+                None if counts is None else cache.check(counts, "counts", torch.int32, (B,)),
+                None if s_new is None else cache.check(s_new, "s_new", torch.float32, (B, n)), ws, ws_bytes)
     return cache
 
 
 def tg_cache_read_q8(cache: CacheQ8, k_out, v_out, first: int = 0, stream=None):
     """Tokens [first, first + n) of every sequence as bf16 into k_out, v_out [B, n, Hkv, d_h] (contiguous);
     rows at or beyond a sequence's length stay as they were."""
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _req(t, name, torch.bfloat16, 4)
-        if (t.shape[0], *t.shape[2:]) != (cache.batch, cache.Hkv, cache.d_h) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{cache.batch}, n, {cache.Hkv}, {cache.d_h}] tensor")
-    if k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out must have one shape")
-    cache.on_device((k_out, "k_out"), (v_out, "v_out"))
-    _check("tg_cache_read_q8", _cache_call(cache, stream, lambda st: lib().tg_cache_read_q8(
-        cache.ref, first, k_out.shape[1], _ptr(k_out), _ptr(v_out), st)))
+    n = k_out.shape[1] if k_out.dim() == 4 else 0
+    shape = (cache.batch, n, cache.Hkv, cache.d_h)
+    _cache_call("tg_cache_read_q8", lib().tg_cache_read_q8, cache, stream, cache.ref, first, n,
+                cache.check(k_out, "k_out", torch.bfloat16, shape), cache.check(v_out, "v_out", torch.bfloat16, shape))
     return k_out, v_out
 
 
@@ -583,21 +596,14 @@ def tg_gated_decode_q8(cache: CacheQ8, q, out, workspace, gain=None, tau: float 
     sequence (query i sees the keys before lengths[b] - (n_q - 1 - i)); out like q; lse [B, n_q, Hq] fp32.
     accumulate adds every key's softmax weight, over queries and heads, to cache.w.  max_len: an upper
     bound on the lengths that sizes the launch (0: the capacity)."""
-    _req(q, "q", torch.bfloat16, 4)
-    _req(out, "out", torch.bfloat16, 4)
-    _req(gain, "gain", torch.float32, 1)
-    _req(lse, "lse", torch.float32, 3)
-    B, n_q, Hq, d_h = q.shape
-    if B != cache.batch or d_h != cache.d_h or out.shape != q.shape or not q.is_contiguous() or not out.is_contiguous():
-        raise ValueError(f"q and out must be contiguous [{cache.batch}, n_q, Hq, {cache.d_h}] tensors")
-    if gain is not None and (gain.shape[0] != Hq or not gain.is_contiguous()):
-        raise ValueError("gain must be a contiguous [Hq] tensor")
-    if lse is not None and (tuple(lse.shape) != (B, n_q, Hq) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous [B, n_q, Hq] tensor")
-    cache.on_device((q, "q"), (out, "out"), (gain, "gain"), (lse, "lse"), (workspace, "workspace"))
-    _check("tg_gated_decode_q8", _cache_call(cache, stream, lambda st: lib().tg_gated_decode_q8(
-        cache.ref, _ptr(q), n_q, Hq, _ptr(gain), tau, 1 if accumulate else 0, max_len, _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel(), st)))
+    B, n_q, Hq, d_h = q.shape if q.dim() == 4 else (cache.batch, 0, 0, cache.d_h)
+    shape = (cache.batch, n_q, Hq, cache.d_h)
+    ws, ws_bytes = _cache_workspace(cache, workspace)
+    _cache_call("tg_gated_decode_q8", lib().tg_gated_decode_q8, cache, stream, cache.ref,
+                cache.check(q, "q", torch.bfloat16, shape), n_q, Hq,
+                None if gain is None else cache.check(gain, "gain", torch.float32, (Hq,)), tau, 1 if accumulate else 0,
+                max_len, cache.check(out, "out", torch.bfloat16, shape),
+                None if lse is None else cache.check(lse, "lse", torch.float32, (B, n_q, Hq)), ws, ws_bytes)
     return out
 
 
@@ -606,12 +612,11 @@ def tg_cache_evict_q8(src: CacheQ8, dst: CacheQ8, kept, workspace, budget: int, 
     """The first `sink`, the last `recent` and the heaviest (by src.w) other tokens of every sequence, `budget` in
     all, into dst in ascending slot order; kept [B, budget] int32 gets their slots in src (-1 behind the last) and
     dst.lengths their number."""
-    _req(kept, "kept", torch.int32, 2)
-    if tuple(kept.shape) != (src.batch, budget) or not kept.is_contiguous():
-        raise ValueError("kept must be a contiguous [B, budget] tensor")
-    src.on_device((dst.k, "dst"), (kept, "kept"), (workspace, "workspace"))
-    _check("tg_cache_evict_q8", _cache_call(src, stream, lambda st: lib().tg_cache_evict_q8(
-        src.ref, dst.ref, budget, sink, recent, max_len, _ptr(kept), _ptr(workspace), workspace.numel(), st)))
+    if dst.index != src.index:
+        raise ValueError(f"dst must be on the cache's device {src.device}")
+    ws, ws_bytes = _cache_workspace(src, workspace)
+    _cache_call("tg_cache_evict_q8", lib().tg_cache_evict_q8, src, stream, src.ref, dst.ref, budget, sink, recent,
+                max_len, src.check(kept, "kept", torch.int32, (src.batch, budget)), ws, ws_bytes)
     return kept
 
 
