@@ -214,17 +214,21 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadAr
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCluster = 8;              // thread blocks that select for one long sequence
-constexpr int kMostKeys = 48 * 1024;     // keys a thread block holds in shared memory
-constexpr int kOneBlockKeys = 16 * 1024; // sequences up to this long are selected by one thread block
+constexpr int kOneBlockKeys = 24 * 1024; // sequences up to this long: one thread block each
+constexpr int kMostKeys = 44 * 1024;     // keys that a thread block's shared memory holds
 
 struct EvictArgs {
     Cache src, dst;
     int64_t budget, sink, recent;
     int32_t* kept;
     unsigned int* status;
-    int cached;                          // keys of a thread block that its shared memory has room for
+    int64_t span;                        // keys that the launch expects of the longest sequence
+    int room;                            // keys that its shared memory holds
 };
 
+__device__ __forceinline__ void cluster_st(void* p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
@@ -256,23 +260,43 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
 }
 
 // CL thread blocks per sequence (one, or a cluster): kept[b, :] ascending, dst's length.  Each thread block owns a
-// contiguous part of the tokens between the sinks and the recent ones (their keys in shared memory where they fit,
-// else read again from L2 each pass), each warp a contiguous part of that.  A sequence is a few KB to a few 100 KB:
-// what bounds the select is the latency of its steps, so a short sequence does without a cluster's barriers.
+// contiguous part of the tokens between the sinks and the recent ones, its keys in shared memory (where they do not
+// fit: read again from L2 each pass), loaded while the sequence's length is still on its way.  A sequence is a few KB
+// to a few 100 KB: what bounds the select is the latency of its steps, and in one SM the instructions a key.  So a short
+// sequence does without a cluster, whose two barriers a pass with the exchange between them take longer than
+// the counting; a thread takes 4 keys at a time; and the loops are short (code that runs once comes from L2
+// too: keys in registers, 24 rounds unrolled, took 1.1 us a pass for 9000 keys).
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t s_key[];
-    __shared__ unsigned s_hist[3][2048];  // one a pass, so that a peer may still read the last one
-    __shared__ unsigned s_scan[4][kSelWarps];
+    extern __shared__ __align__(16) uint32_t s_key[];
+    __shared__ unsigned s_hist[3][2048];  // one a pass: zero from the start
+    __shared__ unsigned s_sum[CL > 1 ? 2048 : 1];   // (the next pass writes it behind a barrier of every reader)
+    __shared__ unsigned s_scan[3][kSelWarps];
     __shared__ unsigned long long s_scan2[kSelWarps];
-    __shared__ unsigned s_pick[3][2], s_cnt[2];
+    __shared__ unsigned s_pick[3][3], s_cnt[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CL > 1 ? cluster_rank_in() : 0;
     for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, sink = static_cast<int>(a.sink), recent = static_cast<int>(a.recent);
     const int n = length_of(a.src, b, a.status);
+    // the keys of this block's part of a span as long as expected (inside the cache, whatever n turns out to be)
+    const int expected = static_cast<int>((a.span + CL - 1) / CL);
+    const float* w = a.src.w + b * a.src.capacity + sink;
+    {
+        const int64_t from = static_cast<int64_t>(rank) * expected, end = a.src.capacity - sink - from;
+        const int most = end < a.room ? static_cast<int>(end) : a.room;
+        for (int i0 = tid; i0 < most; i0 += 8 * kSelThreads) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i0 + kSelThreads * j < most) x[j] = __ldcg(w + from + i0 + kSelThreads * j);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i0 + kSelThreads * j < most) s_key[i0 + kSelThreads * j] = radix_key(x[j]);
+        }
+    }
     int32_t* kept = a.kept + b * a.budget;
     const int gtid = rank * kSelThreads + tid, gthreads = CL * kSelThreads;
     if (gtid == 0) a.dst.lengths[b] = static_cast<int32_t>(n < a.budget ? n : a.budget);
@@ -280,104 +304,112 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
         for (int64_t i = gtid; i < a.budget; i += gthreads) kept[i] = i < n ? static_cast<int32_t>(i) : -1;
         return;
     }
-    const int sink = static_cast<int>(a.sink), recent = static_cast<int>(a.recent);
     const int budget = static_cast<int>(a.budget), kd = budget - sink - recent;
+    // this block's span [c0, c0 + cn) of the m keys, this warp's part [w0, w1) of that in rounds of 128
+    const int m = n - sink - recent;
+    const bool cached = m <= a.span && expected <= a.room;
+    const int per = m <= a.span ? expected : (m + CL - 1) / CL;
+    const int c0 = static_cast<int>(min(static_cast<int64_t>(rank) * per, static_cast<int64_t>(m))), cn = min(per, m - c0);
+    const int rounds = (per + 4 * kSelThreads - 1) / (4 * kSelThreads);
+    const int w0 = min(warp * rounds * 128, cn), w1 = min(w0 + rounds * 128, cn);
+    w += c0;
     for (int i = gtid; i < sink; i += gthreads) kept[i] = i;
     for (int i = gtid; i < recent; i += gthreads) kept[budget - recent + i] = n - recent + i;
     if (kd == 0) return;
-
-    // this block's span [c0, c1) and this warp's part of it
-    const int m = n - sink - recent;
-    const int per = (m + CL - 1) / CL;
-    const int c0 = min(static_cast<int>(rank) * per, m), c1 = min(c0 + per, m), cn = c1 - c0;
-    const int wper = ((per + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int w0 = min(warp * wper, cn), w1 = min(w0 + wper, cn);
-    const float* w = a.src.w + b * a.src.capacity + sink + c0;
-    const bool cached = per <= a.cached;
-    auto key_at = [&](int i) { return cached ? s_key[i] : radix_key(__ldcg(w + i)); };
-    auto count = [&](unsigned* hist, bool match, uint32_t digit) {
-        // one count where a warp's keys agree (ties), else one each
-        const unsigned active = __ballot_sync(0xffffffffu, match);
-        if (match) {
-            int same;
-            __match_all_sync(active, digit, &same);
-            if (!same)
-                atomicAdd(&hist[digit], 1u);
-            else if (lane == __ffs(active) - 1)
-                atomicAdd(&hist[digit], static_cast<unsigned>(__popc(active)));
+    // keys i .. i + 3 (those before `end`; i a multiple of 4)
+    auto four = [&](int i, int end, uint32_t (&k)[4]) {
+        if (cached) {
+            if (i < end) *reinterpret_cast<uint4*>(k) = *reinterpret_cast<const uint4*>(s_key + i);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i + q < end) k[q] = radix_key(__ldcg(w + i + q));
         }
     };
-    __syncthreads();                     // the histograms are zero
+    __syncthreads();                     // the histograms are zero, the keys there
 
     uint32_t prefix = 0, pmask = 0;
     unsigned krem = static_cast<unsigned>(kd);   // rank of the threshold among the keys that match `prefix`
+    bool agree = true;                   // whether many keys match: look for ties
 #pragma unroll 1
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : (p == 1 ? 10 : 0), nb = p == 2 ? 1024 : 2048;
-        for (int i0 = 0; i0 < cn; i0 += 8 * kSelThreads) {
-            uint32_t key[8];
+        for (int i0 = 0; i0 < cn; i0 += 4 * kSelThreads) {
+            const int i = i0 + 4 * tid;
+            uint32_t k[4];
+            four(i, cn, k);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = i0 + j * kSelThreads + tid;
-                key[j] = 0u;
-                if (i < cn) key[j] = p == 0 ? radix_key(__ldcg(w + i)) : key_at(i);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = i0 + j * kSelThreads + tid;
-                if (i0 + j * kSelThreads >= cn) break;
-                if (p == 0 && cached && i < cn) s_key[i] = key[j];
-                count(s_hist[p], i < cn && (key[j] & pmask) == prefix, (key[j] >> shift) & (nb - 1));
+            for (int q = 0; q < 4; ++q) {
+                const bool match = i + q < cn && (k[q] & pmask) == prefix;
+                const uint32_t digit = (k[q] >> shift) & (nb - 1);
+                if (agree) {             // one count where all of a warp's keys agree (ties)
+                    const unsigned active = __ballot_sync(0xffffffffu, match);
+                    const uint32_t first = __shfl_sync(0xffffffffu, digit, active ? __ffs(active) - 1 : 0);
+                    if (__all_sync(0xffffffffu, !match || digit == first)) {
+                        if (lane == 0 && active) atomicAdd(&s_hist[p][first], static_cast<unsigned>(__popc(active)));
+                        continue;
+                    }
+                }
+                if (match) atomicAdd(&s_hist[p][digit], 1u);
             }
         }
-        if (CL > 1) cluster_sync_all();
-        else __syncthreads();
-        // every thread block sums the whole histogram: two bins a thread, from the top digit down
-        unsigned c[2] = {0u, 0u};
+        const unsigned* hist = s_hist[p];
+        if constexpr (CL > 1) {
+            // each thread block adds up an eighth of the bins over the cluster and hands it to all
+            cluster_sync_all();
+            const int sl = nb / CL;
+            if (tid < sl) {
+                const int bin = rank * sl + tid;
+                uint32_t x[CL];
+#pragma unroll
+                for (int r = 0; r < CL; ++r) x[r] = cluster_ld(&s_hist[p][bin], r);
+                uint32_t sum = 0;
+#pragma unroll
+                for (int r = 0; r < CL; ++r) sum += x[r];
+#pragma unroll
+                for (int r = 0; r < CL; ++r) cluster_st(&s_sum[bin], r, sum);
+            }
+            cluster_sync_all();
+            hist = s_sum;
+        } else {
+            __syncthreads();
+        }
+        // two bins a thread, from the top digit down
         const int d0 = nb - 1 - 2 * tid;
-        if (d0 > 0) {
-            if constexpr (CL == 1) {
-                c[0] = s_hist[p][d0];
-                c[1] = s_hist[p][d0 - 1];
-            } else {
-                uint32_t x[2][CL];
-#pragma unroll
-                for (int r = 0; r < CL; ++r) {
-                    x[0][r] = cluster_ld(&s_hist[p][d0], r);
-                    x[1][r] = cluster_ld(&s_hist[p][d0 - 1], r);
-                }
-#pragma unroll
-                for (int r = 0; r < CL; ++r) {
-                    c[0] += x[0][r];
-                    c[1] += x[1][r];
-                }
-            }
-        }
+        const unsigned h0 = d0 > 0 ? hist[d0] : 0u, h1 = d0 > 0 ? hist[d0 - 1] : 0u;
         unsigned tot;
-        const unsigned e = block_scan(c[0] + c[1], s_scan[p], &tot);
-        if (e < krem && krem <= e + c[0]) {
+        const unsigned e = block_scan(h0 + h1, s_scan[p], &tot);
+        if (e < krem && krem <= e + h0) {
             s_pick[p][0] = d0;
             s_pick[p][1] = e;
-        } else if (e + c[0] < krem && krem <= e + c[0] + c[1]) {
+            s_pick[p][2] = h0;
+        } else if (e + h0 < krem && krem <= e + h0 + h1) {
             s_pick[p][0] = d0 - 1;
-            s_pick[p][1] = e + c[0];
+            s_pick[p][1] = e + h0;
+            s_pick[p][2] = h1;
         }
         __syncthreads();
         prefix |= s_pick[p][0] << shift;
         pmask |= static_cast<uint32_t>(nb - 1) << shift;
         krem -= s_pick[p][1];
+        agree = s_pick[p][2] > static_cast<unsigned>(m) / 8;
     }
     // keys above the threshold `prefix` stay, and the first krem equal to it
     unsigned gt = 0, eq = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const bool in = i0 + lane < w1;
-        const uint32_t key = in ? key_at(i0 + lane) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-        eq += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+        uint32_t k[4];
+        four(i, w1, k);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            gt += i + q < w1 && k[q] > prefix;
+            eq += i + q < w1 && k[q] == prefix;
+        }
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     unsigned long long all;
     unsigned long long mine = block_scan(lane == 0 ? static_cast<unsigned long long>(gt) << 32 | eq : 0ull, s_scan2, &all);
-    if (CL > 1) {
+    if constexpr (CL > 1) {
         if (tid == 0) {
             s_cnt[0] = static_cast<unsigned>(all >> 32);
             s_cnt[1] = static_cast<unsigned>(all);
@@ -393,17 +425,28 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
     }
     mine = __shfl_sync(0xffffffffu, mine, 0);
     unsigned gt_before = static_cast<unsigned>(mine >> 32), eq_before = static_cast<unsigned>(mine);
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const bool in = i0 + lane < w1;
-        const uint32_t key = in ? key_at(i0 + lane) : 0u;
-        const unsigned mg = __ballot_sync(0xffffffffu, in && key > prefix);
-        const unsigned me = __ballot_sync(0xffffffffu, in && key == prefix);
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned g = gt_before + __popc(mg & below), q = eq_before + __popc(me & below);
-        const bool keep = in && (key > prefix || (key == prefix && q < krem));
-        if (keep) kept[sink + g + min(q, krem)] = sink + c0 + i0 + lane;
-        gt_before += __popc(mg);
-        eq_before += __popc(me);
+    int32_t* to = kept + sink;
+    auto one = [&](int i) { return i < w1 ? (cached ? s_key[i] : radix_key(__ldcg(w + i))) : 0u; };
+    const unsigned below = (1u << lane) - 1u;
+    if (eq == 0 || eq_before >= krem) {  // none of this warp's equal keys stays
+        to += min(eq_before, krem);
+#pragma unroll 4
+        for (int i = w0 + lane; i < w0 + (w1 - w0 + 31) / 32 * 32; i += 32) {
+            const bool above = i < w1 && one(i) > prefix;
+            const unsigned mg = __ballot_sync(0xffffffffu, above);
+            if (above) to[gt_before + __popc(mg & below)] = sink + c0 + i;
+            gt_before += __popc(mg);
+        }
+    } else {
+        for (int i = w0 + lane; i < w0 + (w1 - w0 + 31) / 32 * 32; i += 32) {
+            const uint32_t k = one(i);
+            const bool above = i < w1 && k > prefix, equal = i < w1 && k == prefix;
+            const unsigned mg = __ballot_sync(0xffffffffu, above), me = __ballot_sync(0xffffffffu, equal);
+            const unsigned g = gt_before + __popc(mg & below), e = eq_before + __popc(me & below);
+            if (above || (equal && e < krem)) to[g + min(e, krem)] = sink + c0 + i;
+            gt_before += __popc(mg);
+            eq_before += __popc(me);
+        }
     }
     if (CL > 1) cluster_sync_all();      // no block leaves while a peer may read its shared memory
 }
@@ -487,17 +530,18 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_evict_gather_kernel(cons
 }
 
 template <int CL>
-static tg_status launch_select(EvictArgs a, int64_t max_len, cudaStream_t st) {
+static tg_status launch_select(EvictArgs a, int64_t keys, cudaStream_t st) {
     static std::atomic<int> smem_set[64];
     auto kern = cache_evict_select_kernel<CL>;
-    constexpr int kMost = (CL == 1 ? kOneBlockKeys : kMostKeys) * 4;
-    if (!set_max_dynamic_smem(kern, kMost, smem_set)) return TG_ERR_CUDA;
-    const int64_t per = (max_len + CL - 1) / CL;
-    a.cached = per * 4 <= kMost ? static_cast<int>(per) : 0;
+    constexpr int kMost = CL == 1 ? kOneBlockKeys : kMostKeys;   // multiples of 4
+    if (!set_max_dynamic_smem(kern, kMost * 4, smem_set)) return TG_ERR_CUDA;
+    a.span = keys > 0 ? keys : 0;
+    const int64_t per = (a.span + CL - 1) / CL;
+    a.room = per <= kMost ? static_cast<int>((per + 3) / 4 * 4) : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL, static_cast<unsigned>(a.src.batch));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.cached) * 4;
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.room) * 4;
     cfg.stream = st;
     cudaLaunchAttribute at[2] = {pdl_attr()};
     at[1].id = cudaLaunchAttributeClusterDimension;
@@ -621,10 +665,8 @@ extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8
     if (max_len == 0 || max_len > src->capacity) max_len = src->capacity;
     cudaStream_t st = as_stream(stream);
     tg_status r;
-    if (max_len <= q8::kOneBlockKeys)
-        r = q8::launch_select<1>(a, max_len, st);
-    else
-        r = q8::launch_select<q8::kCluster>(a, max_len, st);
+    const int64_t keys = max_len - sink - recent;
+    r = keys <= q8::kOneBlockKeys ? q8::launch_select<1>(a, keys, st) : q8::launch_select<q8::kCluster>(a, keys, st);
     if (r != TG_OK || budget == 0) return r;
     const int64_t units = (budget + q8::kBlock - 1) / q8::kBlock * src->Hkv * 2;
     const dim3 grid(static_cast<unsigned>((units + q8::kWarps - 1) / q8::kWarps), static_cast<unsigned>(src->batch));
