@@ -10,9 +10,8 @@
 // Work: a unit is one block (32 keys) of one head of one sequence.  Short caches give every head a thread
 // block of its own.  Else the units of all sequences, in order (sequence, head, block), are cut
 // into equal runs, one for every SM (counted on the device from `lengths`, so one captured
-// launch serves growing and ragged sequences evenly); a run that crosses from one head to the next is
-// shared out among the warps in proportion, so that both heads are read at the same time.  Each warp
-// takes units of its head in turn and keeps its own reference, sum and output; the warps merge in shared memory, and
+// launch serves growing and ragged sequences evenly), and each run into equal parts for its warps, whatever heads
+// they cross.  A warp keeps a reference, a sum and an output of the head it is in; they merge in shared memory, and
 // a second kernel merges the parts of heads that several thread blocks share, in the order of
 // the runs (no atomics: the same bits every time); a third adds up the weights where they are gathered.
 //
@@ -442,57 +441,67 @@ __device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
 // A thread block's part of one head.
 struct Segment {
     int b, kvh, len;
-    int u0, u1;                          // units of the head
-    int w0, w1;                          // the warps that take them
+    unsigned from, to;                   // its units, counted from the run's first
+    int u0;                              // the first of them in the head
     int parts;                           // thread blocks that share the head
     int slot;                            // this thread block's part
 };
 
+// A warp's sums of the segment it is in: the warps' parts and the segments are in the same order, so warp w's
+// sums of segment j are entry w + j.
 template <int D, int NT>
 struct Shared {
     static constexpr int kW = warps_of(NT);
-    float o[kW][8 * NT][D];       // the warps' sums
-    float m[kW][8 * NT], l[kW][8 * NT];
+    float o[2 * kW][8 * NT][D];
+    float m[2 * kW][8 * NT], l[2 * kW][8 * NT];
     Segment seg[kW];
     unsigned red[kW], base, next;
     int n_seg, b;
 };
 
-// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace.
 template <int D, int FMT, int NT, bool kWeights>
-__device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& sh,
-                                            const Warp<D, FMT, NT, kWeights>& wp, int n_seg) {
-    constexpr int kThreads = warps_of(NT) * 32;
-    const int tid = threadIdx.x, warp = tid >> 5;
+__device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh,
+                                          const Warp<D, FMT, NT, kWeights>& wp, int entry) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = 8 * nt + 2 * wp.t + c;
             if (wp.g == 0) {
-                sh.m[warp][r] = wp.m[nt][c];
-                sh.l[warp][r] = wp.l[nt][c];
+                sh.m[entry][r] = wp.m[nt][c];
+                sh.l[entry][r] = wp.l[nt][c];
             }
             if (r < a.R) {
-                float* to = &sh.o[warp][r][D / 8 * wp.g];
+                float* to = &sh.o[entry][r][D / 8 * wp.g];
 #pragma unroll
                 for (int dm = 0; dm < D / 16; ++dm)
                     *reinterpret_cast<float2*>(to + 2 * dm) =
                         make_float2(wp.o[dm][nt][c] * wp.vref, wp.o[dm][nt][2 + c] * wp.vref);
             }
         }
+}
+
+// Merges the warps' sums of the block's segments (`units` in all): whole heads are done, the others' parts go to the
+// workspace.
+template <int D, int NT>
+__device__ __forceinline__ void merge_warps(const DecodeArgs& a, const Shared<D, NT>& sh, int n_seg, unsigned units) {
+    constexpr int kW = warps_of(NT);
     __syncthreads();
-    for (int i = tid; i < n_seg * a.R * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < n_seg * a.R * (D / 4); i += kW * 32) {
         const int jr = i / (D / 4), j = jr / a.R, r = jr % a.R, d = i % (D / 4) * 4;
         const Segment& sg = sh.seg[j];
+        // the warps with the segment's first and last unit
+        const int e0 = j + static_cast<int>(((sg.from + 1ull) * kW - 1) / units);
+        const int e1 = j + static_cast<int>((static_cast<uint64_t>(sg.to) * kW - 1) / units);
         float m = kNothing, l = 0.0f;
-        for (int w = sg.w0; w < sg.w1; ++w) m = fmaxf(m, sh.m[w][r]);
+        for (int e = e0; e <= e1; ++e) m = fmaxf(m, sh.m[e][r]);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int w = sg.w0; w < sg.w1; ++w) {
-            const float f = ex2(sh.m[w][r] - m);
-            l = fmaf(sh.l[w][r], f, l);
-            add4(o, *reinterpret_cast<const float4*>(&sh.o[w][r][d]), f);
+        for (int e = e0; e <= e1; ++e) {
+            const float le = sh.l[e][r], f = ex2(sh.m[e][r] - m);
+            if (le == 0.0f) continue;     // nothing there (a warp without units has no sums either)
+            l = fmaf(le, f, l);
+            add4(o, *reinterpret_cast<const float4*>(&sh.o[e][r][d]), f);
         }
         if (sg.parts == 1) {
             store_out(a.out + out_row(a, sg.b, sg.kvh, r) * D + d, o, l);
@@ -522,11 +531,12 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
     if (a.short_heads) {
         const int b = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv, len = length_of(a.c, b, a.status);
         if (tid == 0) {
-            sh.seg[0] = Segment{b, kvh, len, 0, 0, 0, kW, 1, 0};
+            sh.seg[0] = Segment{b, kvh, len, 0u, kW, 0, 1, 0};
             a.heads[blockIdx.x] = make_int2(0, 0);
         }
         wp.run(b, kvh, warp, (len + kBlock - 1) / kBlock, kW, len);
-        merge_warps<D, FMT, NT, kWeights>(a, sh, wp, 1);
+        keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp);
+        merge_warps<D, NT>(a, sh, 1, kW);   // (as if every warp had had one unit)
         return;
     }
 
@@ -595,9 +605,29 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
     }
     __syncthreads();
 
+    // the thread blocks that hold a head's first and last unit
+    auto parts_of = [&](Segment& sg, unsigned head, unsigned nblk) {
+        const int i0 = static_cast<int>(((head + 1ull) * n - 1) / total);
+        const int i1 = static_cast<int>((static_cast<uint64_t>(head + nblk) * n - 1) / total);
+        sg.parts = i1 - i0 + 1;
+        sg.slot = 2 * blockIdx.x + (head < u_begin ? 0 : 1);
+        if (sg.u0 == 0) a.heads[sg.b * Hkv + sg.kvh] = make_int2(i0, i0 == i1 ? 0 : i1 - i0 + 1);
+    };
     while (u < u_end) {
-        // up to one head a warp: the next segments of the run
-        if (tid == 0) {
+        // the next segments of the run, as many as there are warps
+        if (B == 1) {
+            const int len = length_of(a.c, 0, a.status);
+            const unsigned nblk = (len + kBlock - 1) / kBlock, h = u / nblk + tid, last = (u_end - 1) / nblk;
+            if (tid < kW && h <= last) {
+                const unsigned head = h * nblk, from = max(head, u), to = min(head + nblk, u_end);
+                sh.seg[tid] = Segment{0, static_cast<int>(h), len, from - u, to - u, static_cast<int>(from - head), 0, 0};
+                parts_of(sh.seg[tid], head, nblk);
+                if (tid == kW - 1 || h == last) {
+                    sh.n_seg = tid + 1;
+                    sh.next = to;
+                }
+            }
+        } else if (tid == 0) {
             int k = 0, b = sh.b;
             unsigned base = sh.base, v = u;
             while (v < u_end && k < kW) {
@@ -607,13 +637,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
                     ++b;
                     continue;
                 }
-                const unsigned kvh = (v - base) / nblk, seg = base + kvh * nblk;
-                const unsigned stop = min(seg + nblk, u_end);
-                sh.seg[k] = Segment{b, static_cast<int>(kvh), len, static_cast<int>(v - seg), static_cast<int>(stop - seg),
-                                    0, 0, 1, static_cast<int>(2 * blockIdx.x + (seg < u_begin ? 0 : 1))};
+                const unsigned kvh = (v - base) / nblk, head = base + kvh * nblk, to = min(head + nblk, u_end);
+                sh.seg[k] = Segment{b, static_cast<int>(kvh), len, v - u, to - u, static_cast<int>(v - head), 0, 0};
                 ++k;
-                v = stop;
-                if (v == seg + nblk && kvh == static_cast<unsigned>(Hkv) - 1) {
+                v = to;
+                if (v == head + nblk && kvh == static_cast<unsigned>(Hkv) - 1) {
                     base += nblk * Hkv;
                     ++b;
                 }
@@ -625,37 +653,28 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
         }
         __syncthreads();
         const int n_seg = sh.n_seg;
-        const unsigned u_next = sh.next, spare = kW - n_seg, units = u_next - u;
-        // every segment gets one warp, the others go by its units
-        unsigned seen = 0, my_seen = 0;
-        int my = 0, w0 = 0, w1 = kW;
-        if (n_seg > 1) {
-            for (int j = 0; j < n_seg; ++j) {
-                const int from = j + static_cast<int>(static_cast<uint64_t>(spare) * seen / units);
-                const unsigned c = sh.seg[j].u1 - sh.seg[j].u0;
-                const int to = j + 1 + static_cast<int>(static_cast<uint64_t>(spare) * (seen + c) / units);
-                if (warp >= from && warp < to) {
-                    my = j;
-                    w0 = from;
-                    w1 = to;
-                    my_seen = seen;
-                }
-                seen += c;
-            }
+        const unsigned u_next = sh.next, units = u_next - u;
+        if (B > 1 && tid < n_seg) {
+            Segment& sg = sh.seg[tid];
+            parts_of(sg, u + sg.from - sg.u0, (sg.len + kBlock - 1) / kBlock);
         }
-        Segment& sg = sh.seg[my];
-        if (lane == 0 && warp == w0) {
-            // the thread blocks holding the head's first and last unit
-            const unsigned nblk = (sg.len + kBlock - 1) / kBlock, seg = u + my_seen - sg.u0;
-            const int i0 = static_cast<int>(((seg + 1ull) * n - 1) / total);
-            const int i1 = static_cast<int>((static_cast<uint64_t>(seg + nblk) * n - 1) / total);
-            sg.w0 = w0;
-            sg.w1 = w1;
-            sg.parts = i1 - i0 + 1;
-            if (sg.u0 == 0) a.heads[sg.b * Hkv + sg.kvh] = make_int2(i0, i0 == i1 ? 0 : i1 - i0 + 1);
+        // this warp's units of the run
+        unsigned x = units * warp / kW;
+        const unsigned x_end = units * (warp + 1) / kW;
+        int j = 0;
+        while (j + 1 < n_seg && x >= sh.seg[j].to) ++j;
+        if (x == x_end) {
+            if (lane < 8 * NT) sh.m[warp + j][lane] = kNothing, sh.l[warp + j][lane] = 0.0f;
         }
-        wp.run(sg.b, sg.kvh, sg.u0 + warp - w0, sg.u1, w1 - w0, sg.len);
-        merge_warps<D, FMT, NT, kWeights>(a, sh, wp, n_seg);
+        for (; x < x_end; ++j) {
+            const Segment& sg = sh.seg[j];
+            const unsigned stop = min(sg.to, x_end);
+            const int u0 = sg.u0 + static_cast<int>(x - sg.from);
+            wp.run(sg.b, sg.kvh, u0, u0 + static_cast<int>(stop - x), 1, sg.len);
+            keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp + j);
+            x = stop;
+        }
+        merge_warps<D, NT>(a, sh, n_seg, units);
         __syncthreads();
         u = u_next;
     }
