@@ -13,7 +13,7 @@
 // launch serves growing and ragged sequences evenly), and each run into equal parts for its warps, whatever heads
 // they cross.  A warp keeps a reference, a sum and an output of the head it is in; they merge in shared memory, and
 // a second kernel merges the parts of heads that several thread blocks share, in the order of
-// the runs (no atomics: the same bits every time); a third adds up the weights where they are gathered.
+// the runs (no atomics: the same bits every time), and adds up the weights where they are gathered.
 //
 // A unit in a warp: codes come straight from global memory into registers in the layout of
 // mma.m16n8k16's A operand -- keys (K) or head dimensions (V, transposed by byte permutes) as the
@@ -66,7 +66,7 @@ struct DecodeArgs {
     int short_heads;                     // one thread block a head
     unsigned int* status;
     int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
-    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units
+    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
     float* part;                         // [2 * grid][R][d]: sums of a run's first / last head
     float2* part_ml;                     // [2 * grid][R]: their reference and sum
     float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
@@ -277,7 +277,8 @@ struct Warp {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         *reinterpret_cast<float2*>(to + 8 * r * a.Rp) =
-                            make_float2(x[r >> 1][nt][2 * (r & 1)], x[r >> 1][nt][2 * (r & 1) + 1]);
+                            make_float2(x[r >> 1][nt][2 * (r & 1)],
+                                        8 * nt + 2 * t + 1 < a.R ? x[r >> 1][nt][2 * (r & 1) + 1] : -INFINITY);
                 }
         }
         // the lane's own largest logits against the reference: it rarely has to move
@@ -687,136 +688,191 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
         for (int i = tid; i < a.n_q * a.Hq; i += kThreads)
             if (a.lse) a.lse[static_cast<int64_t>(e) * a.n_q * a.Hq + i] = -INFINITY;
         for (int i = tid; i < Hkv; i += kThreads) a.heads[e * Hkv + i] = make_int2(0, 0);
-        for (int i = tid; i < Hkv * kMaxRows; i += kThreads)
-            a.lse2[static_cast<int64_t>(e) * Hkv * kMaxRows + i] = -INFINITY;
     }
 }
 
-// Merges the parts of heads that several thread blocks share: thread block (h, b), in the order of the parts.
+// Room of a thread block of the second kernel, for either of its tasks.
+constexpr int kMergeVecs = 64, kMergeGroups = kFinThreads / kMergeVecs;   // float4s of the output a thread block merges
+struct MergeRoom {
+    float f[kMaxParts][4], l[4];         // factors and sums of its 2 or 4 rows
+    float4 sum[kMergeGroups][kMergeVecs];
+};
+struct WeightRoom {
+    float lse[64 * kMaxRows];            // infinity in rows that add nothing, the odd last one among them
+    float sum[kWeightTiles][kWeightGroups][kWeightKeys];
+};
+
+// Merges the parts of one head that several thread blocks shared, in the order of the parts: rows r0, r0 + 1, ... (2 of
+// 128 or 4 of 64 numbers).  Groups of threads take the parts in turn; the first of them are under way while the factors
+// form.
 template <int D>
-__global__ void __launch_bounds__(kFinThreads) decode_q8_finish_kernel(const DecodeArgs a) {
-    __shared__ float s_f[kMaxParts][kMaxRows], s_l[kMaxRows];
-    __shared__ float4 s_sum[kFinThreads];
-    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
-    pdl_wait();
-    pdl_trigger();
+__device__ __forceinline__ void merge_parts(const DecodeArgs& a, MergeRoom& room, int b, int h, int r0) {
+    constexpr int kRows = kMergeVecs / (D / 4), kAhead = 6, kPer = kMaxParts / 32;
+    const int tid = threadIdx.x, i = tid % kMergeVecs, grp = tid / kMergeVecs, r = i / (D / 4), d = i % (D / 4) * 4;
     // part p of a head belongs to thread block hd.x + p: its last head for p = 0, its first one otherwise
     const int2 hd = a.heads[b * a.c.Hkv + h];
     auto slot = [&](int p) -> int64_t { return 2 * (hd.x + p) + (p == 0); };
     const int np = hd.y;
     if (np == 0) return;
-            // groups of threads take the parts in turn; the first of them are under way while the factors form
-            const int vecs = a.R * (D / 4), groups = vecs >= kFinThreads ? 1 : kFinThreads / vecs;
-            const int grp = groups > 1 ? tid / vecs : 0;
-            for (int i0 = 0; i0 < vecs; i0 += kFinThreads) {
-                const int i = groups > 1 ? tid % vecs : i0 + tid;
-                const bool active = groups > 1 ? grp < groups : i < vecs;
-                constexpr int kAhead = 10;
-                float4 x[kAhead];
-                const float* from = a.part + static_cast<int64_t>(active ? i : 0) * 4;
-    #pragma unroll
-                for (int y = 0; y < kAhead; ++y)
-                    if (active && grp + y * groups < np)
-                        x[y] = __ldcg(reinterpret_cast<const float4*>(from + slot(grp + y * groups) * a.R * D));
-                if (i0 == 0) {
-                    for (int r = tid / 32; r < a.R; r += kFinThreads / 32) {
-                        constexpr int kPer = kMaxParts / 32;
-                        float2 ml[kPer];
-                        float m = kNothing, l = 0.0f;
-    #pragma unroll
-                        for (int y = 0; y < kPer; ++y) {
-                            const int p = tid % 32 + 32 * y;
-                            ml[y] = p < np ? __ldcg(a.part_ml + slot(p) * a.R + r) : make_float2(kNothing, 0.0f);
-                            m = fmaxf(m, ml[y].x);
-                        }
-    #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    #pragma unroll
-                        for (int y = 0; y < kPer; ++y) {
-                            const float f = ex2(ml[y].x - m);
-                            l = fmaf(ml[y].y, f, l);
-                            if (tid % 32 + 32 * y < np) s_f[tid % 32 + 32 * y][r] = f;
-                        }
-    #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                        if (tid % 32 == 0) {
-                            s_l[r] = l;
-                            const float lse2 = row_lse2(m, l);
-                        a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + h) * kMaxRows + r] = lse2;
-                        if (a.lse) a.lse[out_row(a, b, h, r)] = lse2 * kLn2;
-                        }
-                    }
-                    __syncthreads();
-                }
-                const int r = i / (D / 4), d = i % (D / 4) * 4;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (active) {
-    #pragma unroll
-                    for (int y = 0; y < kAhead; ++y)
-                        if (grp + y * groups < np) add4(o, x[y], s_f[grp + y * groups][r]);
-    #pragma unroll 8
-                    for (int p = grp + kAhead * groups; p < np; p += groups)
-                        add4(o, __ldcg(reinterpret_cast<const float4*>(from + slot(p) * a.R * D)), s_f[p][r]);
-                }
-                if (groups > 1) {
-                    if (active) s_sum[tid] = o;
-                    __syncthreads();
-                    if (tid < vecs) {
-                        for (int y = 1; y < groups; ++y) add4(o, s_sum[y * vecs + tid], 1.0f);
-                        store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
-                    }
-                } else if (active) {
-                    store_out(a.out + out_row(a, b, h, r) * D + d, o, s_l[r]);
-                }
-            }
-}
-
-// w[b, c] += sum over heads and rows of 2^(x - lse2): 64 keys and 4 groups of heads a thread block, up to 4 tiles of
-// keys at once so that many loads are under way, the groups' sums in a fixed order.
-__global__ void __launch_bounds__(kFinThreads) decode_q8_weights_kernel(const DecodeArgs a) {
-    __shared__ float s_lse[64 * kMaxRows];
-    __shared__ float s_sum[kWeightTiles][kWeightGroups][kWeightKeys];
-    const int tid = threadIdx.x, b = blockIdx.y, Hkv = a.c.Hkv, key = tid % kWeightKeys, grp = tid / kWeightKeys;
-    pdl_wait();
-    pdl_trigger();
-    const int len = length_of(a.c, b, a.status);
-    if (static_cast<int64_t>(blockIdx.x) * kWeightKeys >= len) return;
-    for (int i = tid; i < Hkv * a.Rp; i += kFinThreads) {
-        const int h = i / a.Rp, r = i % a.Rp;
-        const float v = r < a.R ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : INFINITY;
-        s_lse[i] = v == -INFINITY ? INFINITY : v;   // a row that saw nothing adds nothing
+    const bool active = r0 + r < a.R;
+    const float* from = a.part + (r0 + r) * D + d;
+    float4 x[kAhead];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int p = p0 + y * kMergeGroups;
+            if (active && p < np) x[y] = __ldcg(reinterpret_cast<const float4*>(from + slot(p) * a.R * D));
+        }
+    };
+    load(grp);
+    const int row = r0 + tid / 32;        // one warp a row
+    if (tid / 32 < kRows && row < a.R) {
+        float2 ml[kPer];
+        float m = kNothing, l = 0.0f;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const int p = tid % 32 + 32 * y;
+            ml[y] = p < np ? __ldcg(a.part_ml + slot(p) * a.R + row) : make_float2(kNothing, 0.0f);
+            m = fmaxf(m, ml[y].x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+            const float f = ex2(ml[y].x - m);
+            l = fmaf(ml[y].y, f, l);
+            if (tid % 32 + 32 * y < np) room.f[tid % 32 + 32 * y][tid / 32] = f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (tid % 32 == 0) {
+            room.l[tid / 32] = l;
+            if (a.lse) a.lse[out_row(a, b, h, row)] = row_lse2(m, l) * kLn2;
+        }
     }
     __syncthreads();
-    const int pairs = a.Rp / 2, items = Hkv * pairs;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWeightKeys;
-    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWeightKeys; c0 < len; c0 += kWeightTiles * stride) {
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = grp; p0 < np; p0 += kAhead * kMergeGroups) {
+        if (p0 > grp) load(p0);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int p = p0 + y * kMergeGroups;
+            if (active && p < np) add4(o, x[y], room.f[p][r]);
+        }
+    }
+    room.sum[grp][i] = o;
+    __syncthreads();
+    if (grp == 0 && active) {
+#pragma unroll
+        for (int y = 1; y < kMergeGroups; ++y) add4(o, room.sum[y][i], 1.0f);
+        store_out(a.out + out_row(a, b, h, r0 + r) * D + d, o, room.l[r]);
+    }
+}
+
+// The weights of keys x * 64, ..., VEC rows of a head at a time.
+template <int VEC>
+__device__ __forceinline__ void add_tiles(const DecodeArgs& a, WeightRoom& room, int b, int x, int nx, int len) {
+    const int tid = threadIdx.x, key = tid % kWeightKeys, grp = tid / kWeightKeys;
+    const int vecs = a.Rp / VEC, items = a.c.Hkv * vecs;
+    const int64_t stride = static_cast<int64_t>(nx) * kWeightKeys;
+    for (int64_t c0 = static_cast<int64_t>(x) * kWeightKeys; c0 < len; c0 += kWeightTiles * stride) {
+        const int64_t c = c0 + key + grp * stride;   // each group finishes one tile
+        float* to = a.c.w + b * a.c.capacity + c;
+        const float before = c < len ? *to : 0.0f;
         float sum[kWeightTiles] = {};
-        const float* x = a.logits + (static_cast<int64_t>(b) * Hkv * a.c.capacity + c0 + key) * a.Rp;
+        const float* from = a.logits + (static_cast<int64_t>(b) * a.c.Hkv * a.c.capacity + c0 + key) * a.Rp;
 #pragma unroll 2
         for (int i = grp; i < items; i += kWeightGroups) {
-            const int h = i / pairs, r = 2 * (i - h * pairs);
-            const float l0 = s_lse[h * a.Rp + r], l1 = s_lse[h * a.Rp + r + 1];
+            const int h = i / vecs, r = (i - h * vecs) * VEC;
+            const float* p = from + h * a.c.capacity * a.Rp + r;
+            float lse[VEC];
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) lse[q] = room.lse[h * a.Rp + r + q];
 #pragma unroll
             for (int j = 0; j < kWeightTiles; ++j)
                 if (c0 + key + j * stride < len) {
-                    const float2 y =
-                        __ldcg(reinterpret_cast<const float2*>(x + (h * a.c.capacity + j * stride) * a.Rp + r));
-                    sum[j] += ex2(y.x - l0);
-                    if (r + 1 < a.R) sum[j] += ex2(y.y - l1);
+                    float y[VEC];
+                    if constexpr (VEC == 4)
+                        *reinterpret_cast<float4*>(y) = __ldcg(reinterpret_cast<const float4*>(p + j * stride * a.Rp));
+                    else
+                        *reinterpret_cast<float2*>(y) = __ldcg(reinterpret_cast<const float2*>(p + j * stride * a.Rp));
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) sum[j] += ex2(y[q] - lse[q]);
                 }
         }
 #pragma unroll
-        for (int j = 0; j < kWeightTiles; ++j) s_sum[j][grp][key] = sum[j];
+        for (int j = 0; j < kWeightTiles; ++j) room.sum[j][grp][key] = sum[j];
         __syncthreads();
-        const int64_t c = c0 + key + grp * stride;   // one group a tile
         if (c < len) {
             float total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWeightGroups; ++i) total += s_sum[grp][i][key];
-            a.c.w[b * a.c.capacity + c] += total;
+            for (int i = 0; i < kWeightGroups; ++i) total += room.sum[grp][i][key];
+            *to = before + total;
         }
         __syncthreads();
     }
+}
+
+// w[b, c] += sum over heads and rows of 2^(x - lse2), thread block x of nx: 64 keys and 4 groups of heads, up to 4 tiles
+// of keys at once so that many loads are under way, the groups' sums in a fixed order.  The log-sum-exps come from
+// the parts themselves, so that this does not wait for their merging.
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& room, int b, int x, int nx) {
+    const int tid = threadIdx.x, Hkv = a.c.Hkv, len = length_of(a.c, b, a.status);
+    if (static_cast<int64_t>(x) * kWeightKeys >= len) return;
+    // 8 lanes a row
+    for (int i = tid / 8; i < (Hkv * a.Rp + 3) / 4 * 4; i += kFinThreads / 8) {
+        const int h = i / a.Rp, r = i % a.Rp;
+        const bool row = h < Hkv && r < a.R;
+        const int2 hd = row ? a.heads[b * Hkv + h] : make_int2(0, 0);
+        float v = row && hd.y == 0 ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : -INFINITY;
+        float m = kNothing, l = 0.0f;
+        for (int p0 = tid % 8; p0 < hd.y; p0 += 32) {
+            float2 ml[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int p = p0 + 8 * y;
+                ml[y] = p < hd.y ? __ldcg(a.part_ml + (2 * (hd.x + p) + (p == 0)) * a.R + r) : make_float2(kNothing, 0.0f);
+            }
+            const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+            l *= ex2(m - mn);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) l = fmaf(ml[y].y, ex2(ml[y].x - mn), l);
+            m = mn;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+            const float mn = fmaxf(m, m2);
+            l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
+            m = mn;
+        }
+        if (hd.y) v = row_lse2(m, l);
+        if (tid % 8 == 0 && h < Hkv) room.lse[i] = v == -INFINITY ? INFINITY : v;   // such a row adds nothing
+    }
+    __syncthreads();
+    if (a.Rp % 4 == 0)
+        add_tiles<4>(a, room, b, x, nx, len);
+    else
+        add_tiles<2>(a, room, b, x, nx, len);
+}
+
+// The second kernel: thread blocks x < merges of sequence b merge its heads' rows, the others add up its weights.
+template <int D>
+__global__ void __launch_bounds__(kFinThreads, 4) decode_q8_finish_kernel(const DecodeArgs a, int merges) {
+    __shared__ union __align__(16) Room {
+        MergeRoom merge;
+        WeightRoom weights;
+        __device__ Room() {}
+    } room;
+    pdl_wait();
+    pdl_trigger();
+    const int x = blockIdx.x, b = blockIdx.y;
+    constexpr int kRows = kMergeVecs / (D / 4);
+    const int chunks = (a.R + kRows - 1) / kRows;
+    if (x < merges)
+        merge_parts<D>(a, room.merge, b, x / chunks, x % chunks * kRows);
+    else
+        add_weights(a, room.weights, b, x - merges, gridDim.x - merges);
 }
 
 // Workspace: status header, heads, lse2, parts, logits (each from a 256-byte boundary).
@@ -916,14 +972,13 @@ extern "C" tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16*
     else
         r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, grid, st)
                                            : q8::launch_rows<64, TG_CACHE_INT8>(a, w, grid, st);
-    const dim3 per_head(static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.c.batch));
-    if (r == TG_OK && !a.short_heads)
-        r = q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>,
-                           per_head, dim3(q8::kFinThreads), 0, st, a);
-    if (r != TG_OK || !w) return r;
-    int64_t x = (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys;
-    if (x > 8 * sms / a.c.batch) x = 8 * sms / a.c.batch;   // (the rest by the kernel's stride)
-    return q8::launch_pdl(q8::decode_q8_weights_kernel,
-                          dim3(static_cast<unsigned>(x < 1 ? 1 : x), static_cast<unsigned>(a.c.batch)),
-                          dim3(q8::kFinThreads), 0, st, a);
+    if (r != TG_OK || (a.short_heads && !w)) return r;
+    int64_t x = w ? (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys : 0;
+    if (x > 4 * sms / a.c.batch) x = 4 * sms / a.c.batch;   // one wave (the rest by the kernel's stride)
+    if (w && x < 1) x = 1;
+    const int rows = q8::kMergeVecs / (cache->d_h / 4);
+    const int merges = a.short_heads ? 0 : a.c.Hkv * ((a.R + rows - 1) / rows);
+    const dim3 fin(static_cast<unsigned>(merges + x), static_cast<unsigned>(a.c.batch));
+    return q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>, fin,
+                          dim3(q8::kFinThreads), 0, st, a, merges);
 }

@@ -335,6 +335,17 @@ def test_decode_masked_keys(fmt):
     assert bool((out[1] == 0).all()) and bool((lse[1] == float("-inf")).all())
 
 
+@pytest.mark.parametrize("Hq,n_q", [(3, 1), (3, 5), (5, 3)])
+def test_decode_odd_rows_with_masked_keys(Hq, n_q):
+    """An odd number of rows a KV head: the row that pads the logits adds no weight, whatever the biases are."""
+    lens = [70]
+    cache, check, nums, s, w, g = random_cache("e4m3", 1, 96, 1, 64, lens, seed=15)
+    s[0, 3:70:4] = float("-inf")
+    cache.s.copy_(s)
+    q = torch.randn(1, n_q, Hq, 64, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, torch.linspace(0.5, 1.5, Hq), 1.0, lens)
+
+
 def test_decode_nan_and_inf_inputs():
     """What the formula makes of them: a NaN key or query gives NaN rows, and only those."""
     lens = [64, 64]
