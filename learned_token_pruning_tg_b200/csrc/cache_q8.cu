@@ -166,46 +166,39 @@ struct ReadArgs {
     Cache c;
     int64_t first, n;
     __nv_bfloat16 *k, *v;
+    int tokens;                          // tokens a thread block takes
 };
 
-// One thread: 16 codes of one token and head, K or V, to 32 bytes.
+// One thread: 8 codes of K and of V to 16 bytes each, so that a warp's loads and stores are runs of memory; a thread
+// block takes `tokens` tokens (about one item a thread: many small thread blocks cover the latency best, 32 tokens a
+// thread block took 1.6 times as long for 16 ragged sequences of up to 840).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.y;
-    int64_t len = __ldg(a.c.lengths + b);
-    if (len > a.c.capacity) len = a.c.capacity;
-    const int64_t rows = (len < a.first + a.n ? len : a.first + a.n) - a.first;
-    const int per_row = a.c.Hkv * (D / 16);
-    const int64_t total = rows * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = i / per_row;
-        const int u = static_cast<int>(i - row * per_row), head = u / (D / 16), col = u % (D / 16) * 16;
-        const int64_t slot = a.first + row;
-        const int64_t from = b * a.c.ld_seq + slot * a.c.ld_token + head * D + col;
-        const int64_t to = ((b * a.n + row) * a.c.Hkv + head) * D + col;
-        const int64_t sc = (b * a.c.blocks() + slot / kBlock) * a.c.Hkv + head;
-        const uint4 ck = __ldg(reinterpret_cast<const uint4*>(a.c.k + from));
-        const uint4 cv = __ldg(reinterpret_cast<const uint4*>(a.c.v + from));
+    const int64_t b = blockIdx.y, row0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    int64_t rows = __ldg(a.c.lengths + b) - a.first;
+    if (rows > a.n) rows = a.n;          // (first + n <= capacity)
+    rows = rows - row0 < a.tokens ? rows - row0 : a.tokens;
+    const int per_row = a.c.Hkv * (D / 8), items = static_cast<int>(rows) * per_row;
+    for (int i = threadIdx.x; i < items; i += kWarps * 32) {
+        const int r = i / per_row, col = (i - r * per_row) * 8;
+        const int64_t slot = a.first + row0 + r;
+        const int64_t from = b * a.c.ld_seq + slot * a.c.ld_token + col;
+        const int64_t sc = (b * a.c.blocks() + slot / kBlock) * a.c.Hkv + col / D;
+        const uint2 ck = __ldg(reinterpret_cast<const uint2*>(a.c.k + from));
+        const uint2 cv = __ldg(reinterpret_cast<const uint2*>(a.c.v + from));
         const float sk = __ldg(a.c.k_scale + sc), sv = __ldg(a.c.v_scale + sc);
+        const int64_t to = (b * a.n + row0) * a.c.Hkv * D + i * 8ll;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const uint4 c = x ? cv : ck;
             const float s = x ? sv : sk;
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f[4];
-                decode4<FMT>(w[j], f);
-                o[2 * j] = pack_bf16x2(f[0] * s, f[1] * s);
-                o[2 * j + 1] = pack_bf16x2(f[2] * s, f[3] * s);
-            }
-            uint4* p = reinterpret_cast<uint4*>((x ? a.v : a.k) + to);
-            p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            float f[4], g[4];
+            decode4<FMT>(x ? cv.x : ck.x, f);
+            decode4<FMT>(x ? cv.y : ck.y, g);
+            *reinterpret_cast<uint4*>((x ? a.v : a.k) + to) =
+                make_uint4(pack_bf16x2(f[0] * s, f[1] * s), pack_bf16x2(f[2] * s, f[3] * s),
+                           pack_bf16x2(g[0] * s, g[1] * s), pack_bf16x2(g[2] * s, g[3] * s));
         }
     }
 }
@@ -623,9 +616,9 @@ extern "C" tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, i
     a.n = n;
     a.k = reinterpret_cast<__nv_bfloat16*>(k_out);
     a.v = reinterpret_cast<__nv_bfloat16*>(v_out);
-    int64_t blocks = (n * a.c.Hkv * (cache->d_h / 16) + q8::kWarps * 32 - 1) / (q8::kWarps * 32);
-    if (blocks > (1 << 20)) blocks = 1 << 20;   // the rest by the kernel's stride
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.c.batch));
+    const int per_row = a.c.Hkv * (cache->d_h / 8);
+    a.tokens = per_row < q8::kWarps * 32 ? q8::kWarps * 32 / per_row : 1;
+    const dim3 grid(static_cast<unsigned>((n + a.tokens - 1) / a.tokens), static_cast<unsigned>(a.c.batch));
     auto kern = cache->d_h == 128 ? (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<128, TG_CACHE_E4M3>
                                                                     : q8::cache_read_q8_kernel<128, TG_CACHE_INT8>)
                                   : (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<64, TG_CACHE_E4M3>
