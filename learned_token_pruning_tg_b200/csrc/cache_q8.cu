@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
     __shared__ unsigned s_sum[CL > 1 ? 2048 : 1];   // (the next pass writes it behind a barrier of every reader)
     __shared__ unsigned s_scan[3][kSelWarps];
     __shared__ unsigned long long s_scan2[kSelWarps];
-    __shared__ unsigned s_pick[3][3], s_cnt[2];
+    __shared__ unsigned s_pick[3][2], s_cnt[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CL > 1 ? cluster_rank_in() : 0;
     for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
 
     uint32_t prefix = 0, pmask = 0;
     unsigned krem = static_cast<unsigned>(kd);   // rank of the threshold among the keys that match `prefix`
-    bool agree = true;                   // whether many keys match: look for ties
 #pragma unroll 1
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : (p == 1 ? 10 : 0), nb = p == 2 ? 1024 : 2048;
@@ -331,19 +330,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
             const int i = i0 + 4 * tid;
             uint32_t k[4];
             four(i, cn, k);
+            bool match[4];
+            uint32_t digit[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const bool match = i + q < cn && (k[q] & pmask) == prefix;
-                const uint32_t digit = (k[q] >> shift) & (nb - 1);
-                if (agree) {             // one count where all of a warp's keys agree (ties)
-                    const unsigned active = __ballot_sync(0xffffffffu, match);
-                    const uint32_t first = __shfl_sync(0xffffffffu, digit, active ? __ffs(active) - 1 : 0);
-                    if (__all_sync(0xffffffffu, !match || digit == first)) {
-                        if (lane == 0 && active) atomicAdd(&s_hist[p][first], static_cast<unsigned>(__popc(active)));
-                        continue;
-                    }
-                }
-                if (match) atomicAdd(&s_hist[p][digit], 1u);
+                match[q] = i + q < cn && (k[q] & pmask) == prefix;
+                digit[q] = (k[q] >> shift) & (nb - 1);
+            }
+            // ties: one count for a thread's four keys
+            const bool same = match[0] && match[1] && match[2] && match[3] && digit[0] == digit[1] &&
+                              digit[0] == digit[2] && digit[0] == digit[3];
+            if (same) {
+                atomicAdd(&s_hist[p][digit[0]], 4u);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (match[q]) atomicAdd(&s_hist[p][digit[q]], 1u);
             }
         }
         const unsigned* hist = s_hist[p];
@@ -375,17 +377,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
         if (e < krem && krem <= e + h0) {
             s_pick[p][0] = d0;
             s_pick[p][1] = e;
-            s_pick[p][2] = h0;
         } else if (e + h0 < krem && krem <= e + h0 + h1) {
             s_pick[p][0] = d0 - 1;
             s_pick[p][1] = e + h0;
-            s_pick[p][2] = h1;
         }
         __syncthreads();
         prefix |= s_pick[p][0] << shift;
         pmask |= static_cast<uint32_t>(nb - 1) << shift;
         krem -= s_pick[p][1];
-        agree = s_pick[p][2] > static_cast<unsigned>(m) / 8;
     }
     // keys above the threshold `prefix` stay, and the first krem equal to it
     unsigned gt = 0, eq = 0;
