@@ -444,6 +444,7 @@ struct Segment {
     int b, kvh, len;
     unsigned from, to;                   // its units, counted from the run's first
     int u0;                              // the first of them in the head
+    int e0, e1;                          // the entries of the warps' sums (below) that are its
     int parts;                           // thread blocks that share the head
     int slot;                            // this thread block's part
 };
@@ -456,7 +457,7 @@ struct Shared {
     float o[2 * kW][8 * NT][D];
     float m[2 * kW][8 * NT], l[2 * kW][8 * NT];
     Segment seg[kW];
-    unsigned red[kW], base, next;
+    unsigned red[kW], base, next, total;
     int n_seg, b;
 };
 
@@ -482,27 +483,30 @@ __device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh
         }
 }
 
-// Merges the warps' sums of the block's segments (`units` in all): whole heads are done, the others' parts go to the
-// workspace.
+// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace.
 template <int D, int NT>
-__device__ __forceinline__ void merge_warps(const DecodeArgs& a, const Shared<D, NT>& sh, int n_seg, unsigned units) {
+__device__ __forceinline__ void merge_warps(const DecodeArgs& a, const Shared<D, NT>& sh, int n_seg) {
     constexpr int kW = warps_of(NT);
     __syncthreads();
     for (int i = threadIdx.x; i < n_seg * a.R * (D / 4); i += kW * 32) {
         const int jr = i / (D / 4), j = jr / a.R, r = jr % a.R, d = i % (D / 4) * 4;
         const Segment& sg = sh.seg[j];
-        // the warps with the segment's first and last unit
-        const int e0 = j + static_cast<int>(((sg.from + 1ull) * kW - 1) / units);
-        const int e1 = j + static_cast<int>((static_cast<uint64_t>(sg.to) * kW - 1) / units);
-        float m = kNothing, l = 0.0f;
-        for (int e = e0; e <= e1; ++e) m = fmaxf(m, sh.m[e][r]);
+        const int e0 = sg.e0, n = sg.e1 - e0;   // n < kW
+        float me[kW], m = kNothing, l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kW; ++e) {
+            me[e] = e <= n ? sh.m[e0 + e][r] : kNothing;
+            m = fmaxf(m, me[e]);
+        }
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int e = e0; e <= e1; ++e) {
-            const float le = sh.l[e][r], f = ex2(sh.m[e][r] - m);
-            if (le == 0.0f) continue;     // nothing there (a warp without units has no sums either)
+#pragma unroll
+        for (int e = 0; e < kW; ++e) {
+            // nothing where a warp saw no key above -inf (one without units has no sums either)
+            const float le = e <= n ? sh.l[e0 + e][r] : 0.0f;
+            if (le == 0.0f) continue;
+            const float f = ex2(me[e] - m);
             l = fmaf(le, f, l);
-            add4(o, *reinterpret_cast<const float4*>(&sh.o[e][r][d]), f);
+            add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), f);
         }
         if (sg.parts == 1) {
             store_out(a.out + out_row(a, sg.b, sg.kvh, r) * D + d, o, l);
@@ -532,12 +536,12 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
     if (a.short_heads) {
         const int b = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv, len = length_of(a.c, b, a.status);
         if (tid == 0) {
-            sh.seg[0] = Segment{b, kvh, len, 0u, kW, 0, 1, 0};
+            sh.seg[0] = Segment{b, kvh, len, 0u, 0u, 0, 0, kW - 1, 1, 0};
             a.heads[blockIdx.x] = make_int2(0, 0);
         }
         wp.run(b, kvh, warp, (len + kBlock - 1) / kBlock, kW, len);
         keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp);
-        merge_warps<D, NT>(a, sh, 1, kW);   // (as if every warp had had one unit)
+        merge_warps<D, NT>(a, sh, 1);
         return;
     }
 
@@ -580,11 +584,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
         u = static_cast<unsigned>(static_cast<uint64_t>(total) * blockIdx.x / n);
         u_end = static_cast<unsigned>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / n);
     }
-    const unsigned u_begin = u;
-    if (tid == 0) {
-        sh.b = 0;
-        sh.base = 0;
-    }
+    if (tid == 0) sh.total = total;
     if (B > 1 && u < u_end) {
         unsigned base = 0;
         for (int b0 = 0;; b0 += kThreads) {
@@ -603,26 +603,18 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
             }
             if (u < base) break;
         }
+        __syncthreads();
     }
-    __syncthreads();
 
-    // the thread blocks that hold a head's first and last unit
-    auto parts_of = [&](Segment& sg, unsigned head, unsigned nblk) {
-        const int i0 = static_cast<int>(((head + 1ull) * n - 1) / total);
-        const int i1 = static_cast<int>((static_cast<uint64_t>(head + nblk) * n - 1) / total);
-        sg.parts = i1 - i0 + 1;
-        sg.slot = 2 * blockIdx.x + (head < u_begin ? 0 : 1);
-        if (sg.u0 == 0) a.heads[sg.b * Hkv + sg.kvh] = make_int2(i0, i0 == i1 ? 0 : i1 - i0 + 1);
-    };
     while (u < u_end) {
-        // the next segments of the run, as many as there are warps
+        // The next segments of the run, as many as there are warps.  One sequence's follow from its length; others
+        // are looked up by one thread.
         if (B == 1) {
             const int len = length_of(a.c, 0, a.status);
             const unsigned nblk = (len + kBlock - 1) / kBlock, h = u / nblk + tid, last = (u_end - 1) / nblk;
             if (tid < kW && h <= last) {
                 const unsigned head = h * nblk, from = max(head, u), to = min(head + nblk, u_end);
-                sh.seg[tid] = Segment{0, static_cast<int>(h), len, from - u, to - u, static_cast<int>(from - head), 0, 0};
-                parts_of(sh.seg[tid], head, nblk);
+                sh.seg[tid] = Segment{0, static_cast<int>(h), len, from - u, to - u, static_cast<int>(from - head)};
                 if (tid == kW - 1 || h == last) {
                     sh.n_seg = tid + 1;
                     sh.next = to;
@@ -639,7 +631,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
                     continue;
                 }
                 const unsigned kvh = (v - base) / nblk, head = base + kvh * nblk, to = min(head + nblk, u_end);
-                sh.seg[k] = Segment{b, static_cast<int>(kvh), len, v - u, to - u, static_cast<int>(v - head), 0, 0};
+                sh.seg[k] = Segment{b, static_cast<int>(kvh), len, v - u, to - u, static_cast<int>(v - head)};
                 ++k;
                 v = to;
                 if (v == head + nblk && kvh == static_cast<unsigned>(Hkv) - 1) {
@@ -653,31 +645,40 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
             sh.next = v;
         }
         __syncthreads();
+        {
+            // this warp's units of the run
+            const unsigned units = sh.next - u;
+            unsigned x = units * warp / kW;
+            const unsigned x_end = units * (warp + 1) / kW;
+            int j = 0;
+            while (j + 1 < sh.n_seg && x >= sh.seg[j].to) ++j;
+            if (x == x_end && lane < 8 * NT) sh.m[warp + j][lane] = kNothing, sh.l[warp + j][lane] = 0.0f;
+            for (; x < x_end; ++j) {
+                const Segment& sg = sh.seg[j];
+                const unsigned stop = min(sg.to, x_end);
+                const int u0 = sg.u0 + static_cast<int>(x - sg.from);
+                wp.run(sg.b, sg.kvh, u0, u0 + static_cast<int>(stop - x), 1, sg.len);
+                keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp + j);
+                x = stop;
+            }
+        }
         const int n_seg = sh.n_seg;
-        const unsigned u_next = sh.next, units = u_next - u;
-        if (B > 1 && tid < n_seg) {
+        if (tid < n_seg) {
+            // the thread blocks with the head's first and last unit, the warps with the segment's
             Segment& sg = sh.seg[tid];
-            parts_of(sg, u + sg.from - sg.u0, (sg.len + kBlock - 1) / kBlock);
+            const unsigned units = sh.next - u, nblk = (sg.len + kBlock - 1) / kBlock, head = u + sg.from - sg.u0;
+            const unsigned total = sh.total, n = min(gridDim.x, total);
+            const int i0 = static_cast<int>(((head + 1ull) * n - 1) / total);
+            const int i1 = static_cast<int>((static_cast<uint64_t>(head + nblk) * n - 1) / total);
+            sg.parts = i1 - i0 + 1;
+            sg.slot = 2 * blockIdx.x + (i0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+            if (sg.u0 == 0) a.heads[sg.b * Hkv + sg.kvh] = make_int2(i0, i0 == i1 ? 0 : i1 - i0 + 1);
+            sg.e0 = tid + static_cast<int>(((sg.from + 1) * kW - 1) / units);
+            sg.e1 = tid + static_cast<int>((sg.to * kW - 1) / units);
         }
-        // this warp's units of the run
-        unsigned x = units * warp / kW;
-        const unsigned x_end = units * (warp + 1) / kW;
-        int j = 0;
-        while (j + 1 < n_seg && x >= sh.seg[j].to) ++j;
-        if (x == x_end) {
-            if (lane < 8 * NT) sh.m[warp + j][lane] = kNothing, sh.l[warp + j][lane] = 0.0f;
-        }
-        for (; x < x_end; ++j) {
-            const Segment& sg = sh.seg[j];
-            const unsigned stop = min(sg.to, x_end);
-            const int u0 = sg.u0 + static_cast<int>(x - sg.from);
-            wp.run(sg.b, sg.kvh, u0, u0 + static_cast<int>(stop - x), 1, sg.len);
-            keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp + j);
-            x = stop;
-        }
-        merge_warps<D, NT>(a, sh, n_seg, units);
+        merge_warps<D, NT>(a, sh, n_seg);
+        u = sh.next;
         __syncthreads();
-        u = u_next;
     }
 
     // sequences without a token have no units: their rows are 0
