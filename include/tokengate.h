@@ -511,8 +511,8 @@ tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16* q, int32_t
  * `recent` tokens stay and, of those between, the budget - sink - recent of
  * largest w (lower slot first on ties, -0 == +0, NaN below every number).
  * Blocks of dst get scales of their own from the values they receive, as an
- * append would give them.  s and w move with their tokens (where both caches have
- * them); dst->lengths[b] = min(n, budget); kept: [batch, budget] int32, the slots
+ * append would give them.  s and w move with their tokens, into the arrays that dst
+ * has (s 0 where src has none); dst->lengths[b] = min(n, budget); kept: [batch, budget] int32, the slots
  * in src, -1 behind the last.  src->w must not be NULL; sink + recent <= budget.
  * max_len: an upper bound on src->lengths that sizes the launch (0 = capacity).
  * Two launches; rows of dst behind its new lengths are left as they were. */

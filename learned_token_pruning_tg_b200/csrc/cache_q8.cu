@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_evict_gather_kernel(cons
     if (lane == 0) (is_v ? a.dst.v_scale : a.dst.k_scale)[(b * a.dst.blocks() + j) * Hkv + head] = scale;
     if (head == 0 && !is_v && slot >= 0) {
         const int64_t at = b * a.dst.capacity + j * kBlock + lane, of = b * a.src.capacity + slot;
-        if (a.dst.s && a.src.s) a.dst.s[at] = a.src.s[of];
+        if (a.dst.s) a.dst.s[at] = a.src.s ? a.src.s[of] : 0.0f;
         if (a.dst.w) a.dst.w[at] = a.src.w[of];
     }
 }
@@ -642,12 +642,15 @@ extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8
         (src->capacity > 0 && !src->w))
         return TG_ERR_INVALID_ARG;
     const size_t sb = q8::code_bytes(a.src, src->d_h), db = q8::code_bytes(a.dst, dst->d_h);
-    const size_t ss = static_cast<size_t>(src->batch) * src->capacity * 4;
-    const size_t ds = static_cast<size_t>(dst->batch) * dst->capacity * 4;
+    const size_t st_bytes = static_cast<size_t>(src->batch) * src->capacity * 4, sc_bytes = st_bytes / q8::kBlock * src->Hkv;
+    const size_t dt_bytes = static_cast<size_t>(dst->batch) * dst->capacity * 4, dc_bytes = dt_bytes / q8::kBlock * dst->Hkv;
+    const size_t len_bytes = static_cast<size_t>(src->batch) * 4;
     if (q8::overlap(src->k, sb, dst->k, db) || q8::overlap(src->v, sb, dst->v, db) ||
         q8::overlap(src->k, sb, dst->v, db) || q8::overlap(src->v, sb, dst->k, db) ||
-        q8::overlap(src->w, ss, dst->w, ds) || q8::overlap(src->s, ss, dst->s, ds) || src->k_scale == dst->k_scale ||
-        src->v_scale == dst->v_scale || src->lengths == dst->lengths)
+        q8::overlap(src->w, st_bytes, dst->w, dt_bytes) || q8::overlap(src->s, st_bytes, dst->s, dt_bytes) ||
+        q8::overlap(src->k_scale, sc_bytes, dst->k_scale, dc_bytes) ||
+        q8::overlap(src->v_scale, sc_bytes, dst->v_scale, dc_bytes) ||
+        q8::overlap(src->lengths, len_bytes, dst->lengths, len_bytes))
         return TG_ERR_INVALID_ARG;
     a.budget = budget;
     a.sink = sink;

@@ -7,13 +7,13 @@
 // The cache is read once: 2 d bytes a key and head, so HBM bounds a long step and latency a
 // short one.
 //
-// Work: a unit is one block (32 keys) of one head of one sequence.  Short caches give every head a thread
-// block of its own.  Else the units of all sequences, in order (sequence, head, block), are cut
-// into equal runs, one for every SM (counted on the device from `lengths`, so one captured
-// launch serves growing and ragged sequences evenly), and each run into equal parts for its warps, whatever heads
-// they cross.  A warp keeps a reference, a sum and an output of the head it is in; they merge in shared memory, and
-// a second kernel merges the parts of heads that several thread blocks share, in the order of
-// the runs (no atomics: the same bits every time), and adds up the weights where they are gathered.
+// Work: a unit is one block (32 keys) of one head of one sequence.  Short caches give every head a thread block, or a
+// cluster of up to 16 of them that merge their sums through distributed shared memory.  Else the units of all
+// sequences, in order (sequence, head, block), are cut into equal runs, one for every SM (counted on the device from
+// `lengths`, so one captured launch serves growing and ragged sequences evenly), and each run into equal
+// parts for its warps, whatever heads they cross.  A warp keeps a reference, a sum and an output of the head it is in;
+// they merge in shared memory, and a second kernel merges the parts of heads that several thread blocks share, in the
+// order of the runs (no atomics: the same bits every time), and adds up the weights where they are gathered.
 //
 // A unit in a warp: codes come straight from global memory into registers in the layout of
 // mma.m16n8k16's A operand -- keys (K) or head dimensions (V, transposed by byte permutes) as the
@@ -43,8 +43,8 @@ namespace q8 {
 constexpr int kDecWarps = 12;
 __host__ __device__ constexpr int warps_of(int NT) { return NT == 1 ? kDecWarps : 8; }
 constexpr int kMaxRows = 16;             // query rows per KV head
+constexpr int kMaxCluster = 16;
 constexpr int kMaxParts = 160;           // thread blocks of a launch that cuts the units into runs
-constexpr int kShortUnits = 2 * kDecWarps;   // heads up to this long get one thread block each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 8.0f;           // weights are 2^(x - m + kShift) ...
@@ -63,7 +63,7 @@ struct DecodeArgs {
     float scale_log2;                    // tau / sqrt(d) * log2(e)
     int n_q, Hq, G, R;
     int Rp;                              // R rounded up to even: a key's logits in the workspace
-    int short_heads;                     // one thread block a head
+    int cluster;                         // thread blocks of a head, as one cluster; 0: runs of units
     unsigned int* status;
     int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
     float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
@@ -71,6 +71,10 @@ struct DecodeArgs {
     float2* part_ml;                     // [2 * grid][R]: their reference and sum
     float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
 };
+
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -439,6 +443,15 @@ __device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
     o.w = fmaf(x.w, f, o.w);
 }
 
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int kvh, int r, int d, int D, float m, float l,
+                                           float4 o) {
+    store_out(a.out + out_row(a, b, kvh, r) * D + d, o, l);
+    if (d != 0) return;
+    const float lse2 = row_lse2(m, l);
+    a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + kvh) * kMaxRows + r] = lse2;
+    if (a.lse) a.lse[out_row(a, b, kvh, r)] = lse2 * kLn2;
+}
+
 // A thread block's part of one head.
 struct Segment {
     int b, kvh, len;
@@ -459,6 +472,9 @@ struct Shared {
     Segment seg[kW];
     unsigned red[kW], base, next, total;
     int n_seg, b;
+    // what the thread blocks of a cluster hand to the one that finishes a number: their sums and references
+    float4 sums[8 * NT * D / 4];
+    float2 ml[kMaxCluster][8 * NT];
 };
 
 template <int D, int FMT, int NT, bool kWeights>
@@ -483,9 +499,19 @@ __device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh
         }
 }
 
-// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace.
+__device__ __forceinline__ void store_cluster(void* to, uint32_t rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr(to, rank)), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_cluster(void* to, uint32_t rank, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(to, rank)), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace, or, in
+// a cluster, to the thread block that finishes them (float4 i of the head is block i % cluster's).
 template <int D, int NT>
-__device__ __forceinline__ void merge_warps(const DecodeArgs& a, const Shared<D, NT>& sh, int n_seg) {
+__device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& sh, int n_seg) {
     constexpr int kW = warps_of(NT);
     __syncthreads();
     for (int i = threadIdx.x; i < n_seg * a.R * (D / 4); i += kW * 32) {
@@ -508,13 +534,12 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, const Shared<D,
             l = fmaf(le, f, l);
             add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), f);
         }
-        if (sg.parts == 1) {
-            store_out(a.out + out_row(a, sg.b, sg.kvh, r) * D + d, o, l);
-            if (d == 0) {
-                const float lse2 = row_lse2(m, l);
-                a.lse2[(static_cast<int64_t>(sg.b) * a.c.Hkv + sg.kvh) * kMaxRows + r] = lse2;
-                if (a.lse) a.lse[out_row(a, sg.b, sg.kvh, r)] = lse2 * kLn2;
-            }
+        if (a.cluster > 1) {
+            const int v = r * (D / 4) + d / 4, rank = cluster_rank_in(), each = a.R * (D / 4) / a.cluster;
+            store_cluster(&sh.sums[rank * each + v / a.cluster], v % a.cluster, o);
+            if (d / 4 < a.cluster) store_cluster(&sh.ml[rank][r], d / 4, make_float2(m, l));
+        } else if (sg.parts == 1) {
+            finish_row(a, sg.b, sg.kvh, r, d, D, m, l, o);
         } else {
             *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(sg.slot) * a.R + r) * D + d) = o;
             if (d == 0) a.part_ml[sg.slot * a.R + r] = make_float2(m, l);
@@ -528,20 +553,43 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
     extern __shared__ __align__(16) uint8_t smem[];
     Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (a.cluster > 1) cluster_arrive();
     pdl_wait();
     pdl_trigger();
     const int B = a.c.batch, Hkv = a.c.Hkv;
     Warp<D, FMT, NT, kWeights> wp(a);
 
-    if (a.short_heads) {
-        const int b = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv, len = length_of(a.c, b, a.status);
+    if (a.cluster) {
+        const int head = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster, b = head / Hkv, kvh = head % Hkv;
+        const int len = length_of(a.c, b, a.status);
         if (tid == 0) {
             sh.seg[0] = Segment{b, kvh, len, 0u, 0u, 0, 0, kW - 1, 1, 0};
-            a.heads[blockIdx.x] = make_int2(0, 0);
+            if (rank == 0) a.heads[head] = make_int2(0, 0);
         }
-        wp.run(b, kvh, warp, (len + kBlock - 1) / kBlock, kW, len);
+        wp.run(b, kvh, rank * kW + warp, (len + kBlock - 1) / kBlock, a.cluster * kW, len);
         keep_sums<D, FMT, NT, kWeights>(a, sh, wp, warp);
+        __syncwarp();
+        if (a.cluster > 1) cluster_wait();   // every thread block of the cluster has begun
         merge_warps<D, NT>(a, sh, 1);
+        if (a.cluster > 1) {
+            __syncwarp();
+            cluster_sync_all();
+            const int each = a.R * (D / 4) / a.cluster;
+            for (int i = tid; i < each; i += kThreads) {
+                const int v = i * a.cluster + rank, r = v / (D / 4), d = v % (D / 4) * 4;
+                float m = kNothing, l = 0.0f;
+                for (int p = 0; p < a.cluster; ++p) m = fmaxf(m, sh.ml[p][r].x);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int p = 0; p < a.cluster; ++p) {
+                    const float2 ml = sh.ml[p][r];
+                    const float f = ex2(ml.x - m);
+                    l = fmaf(ml.y, f, l);
+                    add4(o, sh.sums[p * each + i], f);
+                }
+                finish_row(a, b, kvh, r, d, D, m, l, o);
+            }
+        }
         return;
     }
 
@@ -893,19 +941,75 @@ static Layout layout(const Cache& c, int d_h, int R, bool weights) {
     return L;
 }
 
+// Clusters of `cl` thread blocks that run at the same time (0: none fits), asked for once per kernel and device.
 template <int D, int FMT, int NT, bool kWeights>
-static tg_status launch(const DecodeArgs& a, int grid, cudaStream_t st) {
-    static std::atomic<int> smem_set[64];
+static int max_clusters(int cl) {
+    static std::atomic<int> cache[64][5];
+    const int dev = current_device(), k = cl == 1 ? 0 : cl == 2 ? 1 : cl == 4 ? 2 : cl == 8 ? 3 : 4;
+    if (dev >= 0 && cache[dev][k].load(std::memory_order_acquire)) return cache[dev][k].load() - 1;
     auto kern = gated_decode_q8_kernel<D, FMT, NT, kWeights>;
     constexpr int kSmem = static_cast<int>(sizeof(Shared<D, NT>));
-    if (!set_max_dynamic_smem(kern, kSmem, smem_set)) return TG_ERR_CUDA;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(warps_of(NT) * 32), kSmem, st, a);
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+        (cl <= 8 || cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cl));
+        cfg.blockDim = dim3(warps_of(NT) * 32);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = static_cast<unsigned>(cl);
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    }
+    cudaGetLastError();
+    if (dev >= 0) cache[dev][k].store(n + 1, std::memory_order_release);
+    return n;
+}
+
+// Thread blocks of a head: as many as give every warp one unit, or the most whose clusters all run at the same time;
+// 0 (runs of units) where a warp would have more than 2 units in a thread block alone, or 4 in a cluster.  Returns -1
+// where the kernel cannot be set up.  Measured, cluster against runs, in us: 8 heads of 2 rows, 1025 keys 8.0 (4) to
+// 9.7, 8705 keys 11.5 (8) to 13.1, 12289 keys 14.5 (8) to 14.1; one head of 8 rows, 8705 keys 10.0 (16) to 15.1;
+// 16 heads of 2 rows, 4097 keys 11.5 (4) to 13.3, 12289 keys 22.3 (4) to 20.8.
+template <int D, int FMT, int NT, bool kWeights>
+static int cluster_for(int64_t heads, int64_t blocks) {
+    static std::atomic<int> smem_set[64];
+    if (!set_max_dynamic_smem(gated_decode_q8_kernel<D, FMT, NT, kWeights>, static_cast<int>(sizeof(Shared<D, NT>)), smem_set))
+        return -1;
+    int best = 1;
+    for (int cl = 2; cl <= kMaxCluster && blocks > warps_of(NT) * best; cl *= 2)
+        if (heads * cl <= num_sms() && heads <= max_clusters<D, FMT, NT, kWeights>(cl)) best = cl;
+    return blocks <= (best == 1 ? 2 : 4) * warps_of(NT) * best ? best : 0;
+}
+
+template <int D, int FMT, int NT, bool kWeights>
+static tg_status launch(DecodeArgs& a, int64_t blocks, cudaStream_t st) {
+    const int64_t heads = static_cast<int64_t>(a.c.batch) * a.c.Hkv;
+    a.cluster = cluster_for<D, FMT, NT, kWeights>(heads, blocks);
+    if (a.cluster < 0) return TG_ERR_CUDA;
+    const int64_t sms = num_sms() < kMaxParts ? num_sms() : kMaxParts, grid = a.cluster ? heads * a.cluster : sms;
+    auto kern = gated_decode_q8_kernel<D, FMT, NT, kWeights>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(warps_of(NT) * 32);
+    cfg.dynamicSmemBytes = sizeof(Shared<D, NT>);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2] = {pdl_attr()};
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? launch_status() : TG_ERR_CUDA;
 }
 
 template <int D, int FMT>
-static tg_status launch_rows(const DecodeArgs& a, bool weights, int grid, cudaStream_t st) {
-    if (a.R <= 8) return weights ? launch<D, FMT, 1, true>(a, grid, st) : launch<D, FMT, 1, false>(a, grid, st);
-    return weights ? launch<D, FMT, 2, true>(a, grid, st) : launch<D, FMT, 2, false>(a, grid, st);
+static tg_status launch_rows(DecodeArgs& a, bool weights, int64_t blocks, cudaStream_t st) {
+    if (a.R <= 8) return weights ? launch<D, FMT, 1, true>(a, blocks, st) : launch<D, FMT, 1, false>(a, blocks, st);
+    return weights ? launch<D, FMT, 2, true>(a, blocks, st) : launch<D, FMT, 2, false>(a, blocks, st);
 }
 
 }  // namespace q8
@@ -959,26 +1063,22 @@ extern "C" tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16*
     a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
     a.logits = reinterpret_cast<float*>(ws + L.logits);
     if (max_len == 0 || max_len > a.c.capacity) max_len = a.c.capacity;
-    // one thread block a head where every warp has at most two units of it, else one a SM
-    const int64_t heads = static_cast<int64_t>(a.c.batch) * a.c.Hkv, blocks = (max_len + q8::kBlock - 1) / q8::kBlock;
-    a.short_heads = blocks <= q8::kShortUnits;
-    const int sms = num_sms() < q8::kMaxParts ? num_sms() : q8::kMaxParts;
-    const int grid = static_cast<int>(a.short_heads ? heads : sms);
+    const int64_t blocks = (max_len + q8::kBlock - 1) / q8::kBlock;
     cudaStream_t st = as_stream(stream);
     const bool w = accumulate != 0 && a.c.capacity > 0;
     tg_status r;
     if (cache->d_h == 128)
-        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<128, TG_CACHE_E4M3>(a, w, grid, st)
-                                           : q8::launch_rows<128, TG_CACHE_INT8>(a, w, grid, st);
+        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<128, TG_CACHE_E4M3>(a, w, blocks, st)
+                                           : q8::launch_rows<128, TG_CACHE_INT8>(a, w, blocks, st);
     else
-        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, grid, st)
-                                           : q8::launch_rows<64, TG_CACHE_INT8>(a, w, grid, st);
-    if (r != TG_OK || (a.short_heads && !w)) return r;
+        r = cache->format == TG_CACHE_E4M3 ? q8::launch_rows<64, TG_CACHE_E4M3>(a, w, blocks, st)
+                                           : q8::launch_rows<64, TG_CACHE_INT8>(a, w, blocks, st);
+    if (r != TG_OK || (a.cluster && !w)) return r;
     int64_t x = w ? (max_len + q8::kWeightKeys - 1) / q8::kWeightKeys : 0;
-    if (x > 4 * sms / a.c.batch) x = 4 * sms / a.c.batch;   // one wave (the rest by the kernel's stride)
+    if (x > 4 * num_sms() / a.c.batch) x = 4 * num_sms() / a.c.batch;   // one wave (the rest by the kernel's stride)
     if (w && x < 1) x = 1;
     const int rows = q8::kMergeVecs / (cache->d_h / 4);
-    const int merges = a.short_heads ? 0 : a.c.Hkv * ((a.R + rows - 1) / rows);
+    const int merges = a.cluster ? 0 : a.c.Hkv * ((a.R + rows - 1) / rows);
     const dim3 fin(static_cast<unsigned>(merges + x), static_cast<unsigned>(a.c.batch));
     return q8::launch_pdl(cache->d_h == 128 ? q8::decode_q8_finish_kernel<128> : q8::decode_q8_finish_kernel<64>, fin,
                           dim3(q8::kFinThreads), 0, st, a, merges);

@@ -31,6 +31,7 @@ from typing import Dict, List, Optional
 import torch
 
 from . import tokengate as tg
+from .cache import KVCacheQ8
 
 
 @dataclass(frozen=True)
@@ -195,6 +196,19 @@ class PrunedPrefillStack:
                 x, pos = xk, pk
             x = self._mlp(li, x)
         return x
+
+    def decode_caches(self, extra: int, fmt: str = "e4m3") -> List[KVCacheQ8]:
+        """The keys and values of the last run(keep_kv=True), layer by layer, as 8-bit decode caches with room for
+        `extra` more tokens each: the kept keys' scores are their biases above L (0 below).  Layers with equally many keys share
+        one lengths tensor, so a decoding step advances at most two."""
+        c, caches, lengths = self.cfg, [], {}
+        for k, v, s in self.kv:
+            n = k.shape[0]
+            if n not in lengths:
+                lengths[n] = torch.full((1,), n, dtype=torch.int32, device=self.dev)
+            cache = KVCacheQ8(1, n + extra, c.Hkv, c.d_h, fmt=fmt, lengths=lengths[n], device=self.dev)
+            caches.append(cache.append(k[None], v[None], s=None if s is None else s[None]))
+        return caches
 
     def kv_bytes(self) -> int:
         return sum(k.numel() * k.element_size() + v.numel() * v.element_size() +

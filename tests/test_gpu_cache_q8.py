@@ -308,6 +308,39 @@ def test_decode_parity(fmt, B, lens, Hq, Hkv, d, n_q):
     check_decode(cache, check, nums, s, w, q, gain, 1.3, lens)
 
 
+def spread(n, most, seed):
+    """n lengths between none and `most`, with runs of empty sequences."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(0, most + 1, (n,), generator=g)
+    x[torch.rand(n, generator=g) < 0.2] = 0
+    x[n // 3: n // 3 + 3] = 0
+    x[n // 2] = most
+    return x.tolist()
+
+
+@pytest.mark.parametrize("fmt,B,most,Hq,Hkv,d,n_q", [
+    ("e4m3", 40, 1100, 4, 2, 64, 1),       # more heads than clusters: equal runs over ragged sequences
+    ("int8", 10, 1500, 24, 8, 128, 1),
+    ("int8", 25, 1300, 12, 4, 64, 4),      # 12 rows a head
+    ("e4m3", 400, 850, 1, 1, 64, 1),       # more sequences than threads of a block
+])
+def test_decode_ragged_runs(fmt, B, most, Hq, Hkv, d, n_q):
+    lens = spread(B, most, B)
+    cap = (most + 31) // 32 * 32
+    cache, check, nums, s, w, g = random_cache(fmt, B, cap, Hkv, d, lens, seed=B + most)
+    q = torch.randn(B, n_q, Hq, d, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, 2 * torch.rand(Hq, generator=g), 1.1, lens)
+
+
+@pytest.mark.parametrize("max_len", [1, 400, 800, 1600, 3100, 6200, 0])
+def test_decode_any_launch(max_len):
+    """One, 2, 4, 8 or 16 thread blocks a head, or runs: every launch reads the same caches whole."""
+    lens = [13000, 0, 77]
+    cache, check, nums, s, w, g = random_cache("e4m3", 3, 13024, 1, 64, lens, seed=21)
+    q = torch.randn(3, 2, 3, 64, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, 2 * torch.rand(3, generator=g), 1.1, lens, max_len=max_len)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_decode_without_bias_or_weights_and_any_scale(fmt):
     lens = [300, 45]
@@ -419,6 +452,151 @@ def test_decode_long(fmt, T, Hq, Hkv, n_q):
     # the same bits again (the weights have moved on, nothing else)
     again = cache.decode(q, gain=gain, tau=1.2, accumulate=True)
     assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+# ------------------------------------------------------------------------------------------- a step, captured
+def test_steps_in_a_graph_and_on_streams():
+    """Append and decode captured once and replayed while the sequences grow: the same bits as the calls made one by
+    one on a stream of their own, and as a second graph over another cache, replayed at the same time."""
+    B, H, Hq, d, start, steps = 3, 2, 4, 64, 700, 70      # from one thread block a head into clusters
+    g = torch.Generator(device="cuda").manual_seed(9)
+    first = torch.randn(2, B, start, H, d, generator=g, device="cuda").to(torch.bfloat16)
+    news = torch.randn(steps, 3, B, 1, Hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    bias = torch.randn(steps, B, 1, generator=g, device="cuda")
+    gain = torch.rand(Hq, generator=g, device="cuda")
+    lens0 = ints([start, 0, start - 33])
+
+    def fresh():
+        c = KVCacheQ8(B, start + steps, H, d, fmt="e4m3")
+        c.lengths.copy_(lens0)
+        c.append(first[0], first[1], counts=lens0.clone())
+        c.reserve(1, Hq, True)
+        return c
+
+    def step(c, q, k, v, s, out, lse):
+        c.lengths.add_(1)
+        c.append(k, v, s=s)
+        c.decode(q, out, gain=gain, tau=1.2, lse=lse, accumulate=True)
+
+    eager = fresh()
+    want = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i in range(steps):
+            out, lse = torch.empty(B, 1, Hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(B, 1, Hq, device="cuda")
+            step(eager, news[i, 0], news[i, 1][:, :, :H], news[i, 2][:, :, :H], bias[i], out, lse)
+            want.append((out, lse))
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        c = fresh()
+        q = torch.empty(B, 1, Hq, d, dtype=torch.bfloat16, device="cuda")
+        k, v = (torch.empty(B, 1, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        s, lse = torch.empty(B, 1, device="cuda"), torch.empty(B, 1, Hq, device="cuda")
+        out = torch.empty_like(q)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(c, q, k, v, s, out, lse)
+        graphs.append((graph, c, q, k, v, s, out, lse, torch.cuda.Stream()))
+    for i in range(steps):
+        for graph, c, q, k, v, s, out, lse, stream in graphs:
+            with torch.cuda.stream(stream):
+                q.copy_(news[i, 0])
+                k.copy_(news[i, 1][:, :, :H])
+                v.copy_(news[i, 2][:, :, :H])
+                s.copy_(bias[i])
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, c, q, k, v, s, out, lse, stream in graphs:
+            assert torch.equal(out.view(torch.int16), want[i][0].view(torch.int16)), i
+            assert torch.equal(lse, want[i][1]), i
+    for graph, c, *_ in graphs:
+        for name in ("k", "v", "k_scale", "v_scale", "s", "w", "lengths"):
+            assert np.array_equal(bits(getattr(c, name)), bits(getattr(eager, name))), name
+        assert c.device_status() == 0
+
+
+def test_reserve_before_capture():
+    cache = KVCacheQ8(1, 64, 1, 64)
+    q = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="reserve"):
+        with torch.cuda.graph(graph):
+            cache.decode(q, out)
+    torch.cuda.synchronize()
+    assert bool((cache.decode(q, out) == 0).all())
+
+
+def test_refusals_of_tensors():
+    cache = KVCacheQ8(2, 64, 2, 64)
+    new = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    x = new(2, 1, 2, 64)
+    for bad in (new(2, 1, 2, 64, dt=torch.float16), x.cpu()):
+        with pytest.raises(TypeError):
+            cache.append(bad, x)
+        with pytest.raises(TypeError):
+            cache.decode(bad, out=new(2, 1, 2, 64))
+    for bad in (new(1, 1, 2, 64), new(2, 1, 1, 64), new(2, 1, 2, 128), new(2, 1, 64, 2).transpose(2, 3)):
+        with pytest.raises(ValueError):
+            cache.append(bad, bad)
+    with pytest.raises(ValueError):
+        cache.append(x, new(2, 2, 2, 64))
+    with pytest.raises(ValueError):
+        cache.append(x, x, s=torch.zeros(2, 2, device="cuda"))
+    with pytest.raises(TypeError):
+        cache.append(x, x, counts=torch.ones(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        KVCacheQ8(2, 64, 2, 64, bias=False).append(x, x, s=torch.zeros(2, 1, device="cuda"))
+    with pytest.raises(tg.TokenGateError):
+        KVCacheQ8(2, 64, 2, 64, weights=False).decode(x, accumulate=True)
+    for q in (new(2, 1, 3, 64), new(2, 9, 4, 64)):           # heads, rows a KV head
+        with pytest.raises(tg.TokenGateError):
+            cache.decode(q)
+    with pytest.raises(ValueError):
+        cache.decode(x, out=new(2, 1, 4, 64))
+    with pytest.raises(ValueError):
+        cache.decode(x, gain=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError):
+        cache.read(new(2, 3, 2, 64), new(2, 4, 2, 64))
+    with pytest.raises(tg.TokenGateError):
+        cache.read(new(2, 3, 2, 64), new(2, 3, 2, 64), first=62)
+    with pytest.raises(tg.TokenGateError):
+        cache.evict_into(cache, 32)                          # into itself
+    with pytest.raises(tg.TokenGateError):
+        cache.evict_into(KVCacheQ8(2, 32, 2, 64), 32, sink=20, recent=20)
+    with pytest.raises(tg.TokenGateError):
+        cache.evict_into(KVCacheQ8(2, 32, 2, 64, fmt="int8"), 32)
+    base = new(2, 64, 2, 65, dt=torch.int8)[..., :64]
+    with pytest.raises(ValueError, match="dense"):
+        KVCacheQ8.over(base, base, torch.ones(2, 2, 2, device="cuda"), torch.ones(2, 2, 2, device="cuda"), ints([0, 0]))
+
+
+def test_strided_cache():
+    """K and V as views of one buffer (tokens of K and V codes side by side), sequences with room between them."""
+    B, cap, H, d = 2, 64, 2, 64
+    g = torch.Generator().manual_seed(4)
+    buf = torch.full((B, cap + 32, 2, H, d), 0x7f, dtype=torch.uint8, device="cuda")
+    k, v = (buf[:, :cap, i].view(torch.int8) for i in range(2))
+    lens = [50, 64]
+    cache = KVCacheQ8.over(k, v, torch.zeros(B, 2, H, device="cuda"), torch.zeros(B, 2, H, device="cuda"), ints(lens),
+                           w=torch.zeros(B, cap, device="cuda"))
+    x = torch.randn(2, B, 64, H, d, generator=g).to(torch.bfloat16)
+    cache.append(x[0].cuda(), x[1].cuda(), counts=ints(lens))
+    q = torch.randn(B, 1, 4, d, generator=g).to(torch.bfloat16)
+    nums = {m: ref.values(ref.code_values(t), sc.double().cpu().numpy())
+            for m, t, sc in (("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale))}
+    check_decode(cache, lambda: None, nums, None, torch.zeros(B, cap), q, None, 1.0, lens)
+    dst = KVCacheQ8(B, 32, H, d, fmt="int8")
+    kept = cache.evict_into(dst, 20, sink=1, recent=2)
+    for b in range(B):
+        want, scale = ref.append(np.zeros((1, 32, H, d)), np.ones((1, 1, H)), [20], [20],
+                                 nums["v"][b: b + 1, kept[b].tolist()], "int8")
+        same_numbers(dst.v[b: b + 1], want)
+    assert bool((buf[:, cap:] == 0x7f).all()) and bool((buf[0, 50:cap] == 0x7f).all())
+    assert bool((dst.s[:, :20] == 0).all())
 
 
 # ------------------------------------------------------------------------------------------- eviction
