@@ -77,7 +77,7 @@ class KVCacheQ8:
                counts: Optional[torch.Tensor] = None) -> "KVCacheQ8":
         """tg_cache_append_q8: k, v [B, n, Hkv, d_h] bf16 become the last tokens of every sequence; `lengths`
         hold the tokens after the append."""
-        tg.tg_cache_append_q8(self.handle, k, v, self._workspace, s_new=s, counts=counts)
+        tg.tg_cache_append_q8(self.handle, k, v, self._workspace, s, counts)
         return self
 
     def decode(self, q: torch.Tensor, out: Optional[torch.Tensor] = None, gain: Optional[torch.Tensor] = None,

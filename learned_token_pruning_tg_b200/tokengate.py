@@ -511,6 +511,7 @@ class CacheQ8:
         self.k, self.v, self.k_scale, self.v_scale, self.lengths, self.s, self.w = k, v, k_scale, v_scale, lengths, s, w
         self.batch, self.capacity, self.Hkv, self.d_h, self.format, self.device = B, cap, Hkv, d_h, fmt, k.device
         self.index = k.get_device()
+        lib()                                        # a missing library shows here
         p = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
         self.struct = CacheStruct(fmt, B, Hkv, d_h, cap, ld_token, ld_seq, p(k), p(v), p(k_scale), p(v_scale),
                                   p(lengths), p(s), p(w))
@@ -531,13 +532,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _cache_call(name, fn, cache, stream, *args):
-    """fn(*args, stream pointer) with the cache's device current."""
+def _cache_call(name, cache, stream, call):
+    """`call(stream pointer)` with the cache's device current."""
     if torch.cuda.current_device() == cache.index:
-        status = fn(*args, _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+        status = call(_raw_stream(cache.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(cache.index):
-            status = fn(*args, _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+            status = call(_raw_stream(cache.index) if stream is None else stream.cuda_stream)
     if status != TG_OK:
         raise TokenGateError(name, status)
 
@@ -556,27 +557,31 @@ def tg_cache_append_q8(cache: CacheQ8, k, v, workspace, s_new=None, counts=None,
     """Appends k, v [B, n, Hkv, d_h] bf16 (heads dense; token and sequence strides free) as the last tokens of
     every sequence: token i to slot lengths[b] - counts[b] + i (counts [B] int32; None: n each), so
     cache.lengths hold the tokens after the append.  s_new: [B, n] fp32 biases."""
-    B, Hkv, d_h = cache.batch, cache.Hkv, cache.d_h
-    row = Hkv * d_h
-    n = k.shape[1] if k.dim() == 4 else 0
-    lds = []
-    for t, name in ((k, "k"), (v, "v")):
-        if t.dtype is not torch.bfloat16 or t.get_device() != cache.index or t.shape != (B, n, Hkv, d_h):
+    B, Hkv, d_h, index = cache.batch, cache.Hkv, cache.d_h, cache.index
+    shape = k.shape
+    if not (k.dtype is v.dtype is torch.bfloat16 and k.get_device() == v.get_device() == index and len(shape) == 4
+            and shape[0] == B and shape[2] == Hkv and shape[3] == d_h and v.shape == shape):
+        for t, name in ((k, "k"), (v, "v")):
             _req(t, name, torch.bfloat16, 4)
-            if t.get_device() != cache.index:
+            if t.get_device() != index:
                 raise ValueError(f"{name} must be on the cache's device {cache.device}")
-            raise ValueError(f"k and v must be [{B}, n, {Hkv}, {d_h}]")
-        sb, st, sh, sd = t.stride()
-        if (sd != 1 or (sh != d_h and Hkv > 1)) and t.numel():
-            raise ValueError(f"{name}: heads must be dense in a token")
-        ld = st if n > 1 else row
-        lds.append((t.data_ptr(), ld, sb if B > 1 else ld * max(n, 1)))
+        raise ValueError(f"k and v must be [{B}, n, {Hkv}, {d_h}]")
+    n = shape[1]
+    kb, kt, kh, kd = k.stride()
+    vb, vt, vh, vd = v.stride()
+    if not (kd == vd == 1 and (Hkv == 1 or kh == vh == d_h)) and k.numel():
+        raise ValueError("k and v: heads must be dense in a token")
+    if n <= 1:                                       # strides of dimensions of one entry say nothing
+        kt = vt = Hkv * d_h
+    if B <= 1:
+        kb, vb = kt * n, vt * n
     if s_new is not None and cache.s is None:
         raise ValueError("s_new is for a cache with s")
     ws, ws_bytes = _cache_workspace(cache, workspace)
-    _cache_call("tg_cache_append_q8", lib().tg_cache_append_q8, cache, stream, cache.ref, *lds[0], *lds[1], n,
-                None if counts is None else cache.check(counts, "counts", torch.int32, (B,)),
-                None if s_new is None else cache.check(s_new, "s_new", torch.float32, (B, n)), ws, ws_bytes)
+    counts = None if counts is None else cache.check(counts, "counts", torch.int32, (B,))
+    s_new = None if s_new is None else cache.check(s_new, "s_new", torch.float32, (B, n))
+    _cache_call("tg_cache_append_q8", cache, stream, lambda st: _lib.tg_cache_append_q8(
+        cache.ref, k.data_ptr(), kt, kb, v.data_ptr(), vt, vb, n, counts, s_new, ws, ws_bytes, st))
     return cache
 
 
@@ -585,8 +590,9 @@ def tg_cache_read_q8(cache: CacheQ8, k_out, v_out, first: int = 0, stream=None):
     rows at or beyond a sequence's length stay as they were."""
     n = k_out.shape[1] if k_out.dim() == 4 else 0
     shape = (cache.batch, n, cache.Hkv, cache.d_h)
-    _cache_call("tg_cache_read_q8", lib().tg_cache_read_q8, cache, stream, cache.ref, first, n,
-                cache.check(k_out, "k_out", torch.bfloat16, shape), cache.check(v_out, "v_out", torch.bfloat16, shape))
+    kp, vp = cache.check(k_out, "k_out", torch.bfloat16, shape), cache.check(v_out, "v_out", torch.bfloat16, shape)
+    _cache_call("tg_cache_read_q8", cache, stream,
+                lambda st: _lib.tg_cache_read_q8(cache.ref, first, n, kp, vp, st))
     return k_out, v_out
 
 
@@ -596,14 +602,17 @@ def tg_gated_decode_q8(cache: CacheQ8, q, out, workspace, gain=None, tau: float 
     sequence (query i sees the keys before lengths[b] - (n_q - 1 - i)); out like q; lse [B, n_q, Hq] fp32.
     accumulate adds every key's softmax weight, over queries and heads, to cache.w.  max_len: an upper
     bound on the lengths that sizes the launch (0: the capacity)."""
-    B, n_q, Hq, d_h = q.shape if q.dim() == 4 else (cache.batch, 0, 0, cache.d_h)
-    shape = (cache.batch, n_q, Hq, cache.d_h)
+    shape = q.shape
+    B, n_q, Hq = shape[:3] if len(shape) == 4 else (cache.batch, 0, 0)
+    if B != cache.batch or len(shape) != 4 or shape[3] != cache.d_h:
+        _req(q, "q", torch.bfloat16, 4)
+        raise ValueError(f"q must be [{cache.batch}, n_q, Hq, {cache.d_h}]")
+    qp, op = cache.check(q, "q", torch.bfloat16, shape), cache.check(out, "out", torch.bfloat16, shape)
+    gp = None if gain is None else cache.check(gain, "gain", torch.float32, (Hq,))
+    lp = None if lse is None else cache.check(lse, "lse", torch.float32, (B, n_q, Hq))
     ws, ws_bytes = _cache_workspace(cache, workspace)
-    _cache_call("tg_gated_decode_q8", lib().tg_gated_decode_q8, cache, stream, cache.ref,
-                cache.check(q, "q", torch.bfloat16, shape), n_q, Hq,
-                None if gain is None else cache.check(gain, "gain", torch.float32, (Hq,)), tau, 1 if accumulate else 0,
-                max_len, cache.check(out, "out", torch.bfloat16, shape),
-                None if lse is None else cache.check(lse, "lse", torch.float32, (B, n_q, Hq)), ws, ws_bytes)
+    _cache_call("tg_gated_decode_q8", cache, stream, lambda st: _lib.tg_gated_decode_q8(
+        cache.ref, qp, n_q, Hq, gp, tau, accumulate, max_len, op, lp, ws, ws_bytes, st))
     return out
 
 
@@ -615,8 +624,9 @@ def tg_cache_evict_q8(src: CacheQ8, dst: CacheQ8, kept, workspace, budget: int, 
     if dst.index != src.index:
         raise ValueError(f"dst must be on the cache's device {src.device}")
     ws, ws_bytes = _cache_workspace(src, workspace)
-    _cache_call("tg_cache_evict_q8", lib().tg_cache_evict_q8, src, stream, src.ref, dst.ref, budget, sink, recent,
-                max_len, src.check(kept, "kept", torch.int32, (src.batch, budget)), ws, ws_bytes)
+    kp = src.check(kept, "kept", torch.int32, (src.batch, budget))
+    _cache_call("tg_cache_evict_q8", src, stream, lambda st: _lib.tg_cache_evict_q8(
+        src.ref, dst.ref, budget, sink, recent, max_len, kp, ws, ws_bytes, st))
     return kept
 
 
