@@ -455,8 +455,8 @@ typedef struct {
 
 /* Workspace bytes for the cache calls with n_q queries a sequence of Hq heads
  * each (n_q = Hq = 0: append, evict and read only; accumulate: whether
- * tg_gated_decode_q8 will gather weights).  0 for bad arguments.  Zero-fill it
- * once; concurrent calls must not share one. */
+ * tg_gated_decode_q8 will gather weights).  0 for bad arguments.  Zero-fill its
+ * first 256 bytes (the status word) once; concurrent calls must not share one. */
 size_t tg_cache_workspace_bytes(const tg_cache_q8* cache, int32_t n_q, int32_t Hq, int32_t accumulate);
 
 /* Appends counts[b] tokens (n_new where counts is NULL) to every sequence, as

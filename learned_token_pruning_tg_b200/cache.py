@@ -69,7 +69,8 @@ class KVCacheQ8:
                     raise RuntimeError("call reserve() before capturing a decode of this shape")
                 if self._workspace is not None:
                     self._retired.append(self._workspace)   # a captured graph may still use it
-                self._workspace = torch.zeros(n, dtype=torch.uint8, device=self.handle.device)
+                self._workspace = torch.empty(n, dtype=torch.uint8, device=self.handle.device)
+                self._workspace[:256].zero_()               # the status word; the rest is written before it is read
             self._room[key] = n
         return self._workspace
 
