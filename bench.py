@@ -734,6 +734,36 @@ def run_stack(args, rank, world, local_rank):
             "clocks": clk.summary(), "device_status": status}
 
 
+class DecodeLayerCache:
+    """One layer's random cache of T keys with scores, in bf16 for tg_gated_decode or in 8 bits for tg_gated_decode_q8."""
+
+    def __init__(self, fmt, T, Hq, Hkv, d_h, gen, dev):
+        from learned_token_pruning_tg_b200 import tokengate as tg
+        from learned_token_pruning_tg_b200.cache import KVCacheQ8
+        self.fmt, self.T, self.tg = fmt, T, tg
+        self.k, self.v = (torch.randn(T, Hkv, d_h, generator=gen, device=dev, dtype=torch.bfloat16) for _ in range(2))
+        self.s = torch.randn(T, generator=gen, device=dev)
+        self.bytes, self.score_bytes = 2 * self.k.numel() * self.k.element_size(), 4 * T
+        if fmt != "bf16":
+            self.q8 = KVCacheQ8(1, T, Hkv, d_h, fmt=fmt, weights=False, device=dev)
+            self.q8.lengths.fill_(T)
+            self.q8.append(self.k[None], self.v[None], s=self.s[None])
+            self.q8.reserve(1, Hq)
+            self.k = self.v = None
+            self.bytes = self.bytes // 2 + 2 * -(-T // tg.TG_CACHE_BLOCK) * Hkv * 4
+
+    def decode(self, q, out, ws, gain=None, tau=1.0):
+        """gain None: the keys' scores are left out."""
+        if self.fmt != "bf16":
+            self.q8.decode(q[None, None], out[None, None], gain=gain, tau=tau, max_len=self.T)
+        else:
+            self.tg.tg_gated_decode(q, self.k, self.v, out, ws, s_cache=None if gain is None else self.s, gain=gain,
+                                    tau=tau)
+
+    def status(self):
+        return 0 if self.fmt == "bf16" else self.q8.device_status()
+
+
 def run_decode(args, rank, world, local_rank):
     """One decoding step's attention over the KV cache a 28-layer 64k pruned prefill leaves (layers
     up to the gate layer hold all N keys, the layers above the K kept keys with their scores; plus
@@ -750,9 +780,7 @@ def run_decode(args, rank, world, local_rank):
     gen.manual_seed(cfg.seed + 7 + rank)
 
     def cache(T):
-        return (torch.randn(T, Hkv, d_h, generator=gen, device=dev, dtype=torch.bfloat16),
-                torch.randn(T, Hkv, d_h, generator=gen, device=dev, dtype=torch.bfloat16),
-                torch.randn(T, generator=gen, device=dev))
+        return DecodeLayerCache(args.cache, T, Hq, Hkv, d_h, gen, dev)
 
     T_all, T_kept = cfg.N + 1, cfg.K + 1
     pruned = [cache(T_all if li <= L else T_kept) for li in range(cfg.n_layers)]
@@ -763,15 +791,14 @@ def run_decode(args, rank, world, local_rank):
     ws = tg.new_workspace(0, Hq, op=tg.TG_OP_DECODE, device=dev)
 
     def step(layers, prune):
-        for li, (k, v, sc) in enumerate(layers):
+        for li, layer in enumerate(layers):
             if prune and li > L:
-                tg.tg_gated_decode(q, k, v, out, ws, s_cache=sc, gain=gain, tau=1.1)
+                layer.decode(q, out, ws, gain=gain, tau=1.1)
             else:
-                tg.tg_gated_decode(q, k, v, out, ws, tau=1.0)
+                layer.decode(q, out, ws)
 
     def cache_bytes(layers, prune):
-        return sum(k.numel() * 2 * 2 + (sc.numel() * 4 if prune and li > L else 0)
-                   for li, (k, v, sc) in enumerate(layers))
+        return sum(layer.bytes + (layer.score_bytes if prune and li > L else 0) for li, layer in enumerate(layers))
 
     reps = max(10, min(args.steps, 200))
 
@@ -802,6 +829,8 @@ def run_decode(args, rank, world, local_rank):
         ms_pruned = timed(pruned, True)
         ms_dense = timed(dense, False)
     status = tg.tg_device_status(ws)
+    for layer in pruned + dense:
+        status |= layer.status()
     if rank != 0:
         return None
     peaks = load_peaks()
@@ -811,14 +840,15 @@ def run_decode(args, rank, world, local_rank):
                       f"pruned prefill (gate after layer {cfg.gate_layer}, {cfg.k_doc} document tokens kept)",
             "value": ms_pruned, "unit": "ms", "n_gpus": world, "steps": reps, "warmup": args.warmup,
             "ms_per_step": ms_pruned, "higher_is_better": False, "scaling": "weak", "vs_baseline": None,
-            "dtype": "bf16", "data": "synthetic (seeded random caches)",
-            "config": {"workload": f"{cfg.name} decode", "layers": cfg.n_layers, "gate_layer": L,
+            "dtype": args.cache, "data": "synthetic (seeded random caches)",
+            "config": {"workload": f"{cfg.name} decode", "cache": args.cache, "layers": cfg.n_layers, "gate_layer": L,
                        "keys_per_layer": {"up_to_gate": T_all, "above_gate": T_kept}, "Hq": Hq, "Hkv": Hkv,
                        "d_h": d_h, "timing": "one CUDA graph of the 28 launches per step, replayed"},
             "impl": "tokengate", "dense_ms": ms_dense, "speedup": ms_dense / ms_pruned,
             "bytes_per_step": {"pruned": b_pruned, "dense": b_dense},
             "roofline": {"bound": "hbm", "achieved": achieved, "peak": peaks["hbm_gbs"], "unit": "GB/s",
-                         "frac": achieved / peaks["hbm_gbs"], "traffic": None, "kernel": "gated_decode_kernel",
+                         "frac": achieved / peaks["hbm_gbs"], "traffic": None,
+                         "kernel": "gated_decode_kernel" if args.cache == "bf16" else "gated_decode_q8_kernel",
                          "dense_frac": b_dense / (ms_dense * 1e-3) / 1e9 / peaks["hbm_gbs"]},
             "gpu_launches": cfg.n_layers * reps, "clocks": clk.summary(), "device_status": status,
             **decode_cpu_baseline(args, [T_all if li <= L else T_kept for li in range(cfg.n_layers)], Hq, Hkv,
@@ -836,39 +866,38 @@ def run_decode_layer(args, rank, world, local_rank):
     T = cfg.N + 1
     gen = torch.Generator(device=dev)
     gen.manual_seed(cfg.seed + 11 + rank)
-    k = torch.randn(T, cfg.Hkv, cfg.d_h, generator=gen, device=dev, dtype=torch.bfloat16)
-    v = torch.randn(T, cfg.Hkv, cfg.d_h, generator=gen, device=dev, dtype=torch.bfloat16)
-    s = torch.randn(T, generator=gen, device=dev)
+    layer = DecodeLayerCache(args.cache, T, cfg.Hq, cfg.Hkv, cfg.d_h, gen, dev)
     q = torch.randn(cfg.Hq, cfg.d_h, generator=gen, device=dev, dtype=torch.bfloat16)
     gain = 2.0 * torch.rand(cfg.Hq, generator=gen, device=dev)
     out = torch.empty(cfg.Hq, cfg.d_h, dtype=torch.bfloat16, device=dev)
     ws = tg.new_workspace(0, cfg.Hq, op=tg.TG_OP_DECODE, device=dev)
     for _ in range(max(3, args.warmup)):
-        tg.tg_gated_decode(q, k, v, out, ws, s_cache=s, gain=gain, tau=1.1)
+        layer.decode(q, out, ws, gain=gain, tau=1.1)
     torch.cuda.synchronize()
     reps = max(3, min(args.steps, 100))
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     e0.record()
     for _ in range(reps):
-        tg.tg_gated_decode(q, k, v, out, ws, s_cache=s, gain=gain, tau=1.1)
+        layer.decode(q, out, ws, gain=gain, tau=1.1)
     e1.record()
     torch.cuda.synchronize()
     us = reduce_max(e0.elapsed_time(e1) / reps * 1e3, dev)
     if rank != 0:
         return None
-    nbytes = 2 * k.numel() * 2 + s.numel() * 4
+    nbytes = layer.bytes + layer.score_bytes
     peaks = load_peaks()
     gbs = nbytes / (us * 1e-6) / 1e9
     return {"metric": "one layer's decoding-step attention over a 64k KV cache", "value": us, "unit": "us",
             "n_gpus": world, "steps": reps, "warmup": args.warmup, "ms_per_step": us / 1e3,
-            "higher_is_better": False, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+            "higher_is_better": False, "scaling": "weak", "vs_baseline": None, "dtype": args.cache,
             "data": "synthetic (seeded random cache)",
-            "config": {"workload": "qwen3-1.7b 64k layer cache", "T": T, "Hq": cfg.Hq, "Hkv": cfg.Hkv, "d_h": cfg.d_h,
-                       "l2": "cache 268 MB > L2, no flush"},
+            "config": {"workload": "qwen3-1.7b 64k layer cache", "cache": args.cache, "T": T, "Hq": cfg.Hq, "Hkv": cfg.Hkv, "d_h": cfg.d_h,
+                       "l2": f"cache {nbytes / 1e6:.0f} MB > L2, no flush"},
             "impl": "tokengate",
             "roofline": {"bound": "hbm", "achieved": gbs, "peak": peaks["hbm_gbs"], "unit": "GB/s",
-                         "frac": gbs / peaks["hbm_gbs"], "traffic": None, "kernel": "gated_decode_kernel"},
-            "gpu_launches": reps, "device_status": tg.tg_device_status(ws),
+                         "frac": gbs / peaks["hbm_gbs"], "traffic": None,
+                         "kernel": "gated_decode_kernel" if args.cache == "bf16" else "gated_decode_q8_kernel"},
+            "gpu_launches": reps, "device_status": tg.tg_device_status(ws) | layer.status(),
             **decode_cpu_baseline(args, [T], cfg.Hq, cfg.Hkv, cfg.d_h, 1e6, "us")}
 
 
@@ -958,6 +987,8 @@ def main():
                     help="time one layer's decoding step over a 64k cache (the decode kernel alone)")
     ap.add_argument("--decode", action="store_true",
                     help="time one decoding step's attention over a pruned 28-layer cache (and an unpruned one)")
+    ap.add_argument("--cache", choices=["bf16", "e4m3", "int8"], default="bf16",
+                    help="how --decode and --decode-layer hold the cache")
     ap.add_argument("--backward", action="store_true",
                     help="time the gated attention backward at the 128k workload's kept set")
     ap.add_argument("--stack", action="store_true",
