@@ -98,7 +98,8 @@ class KVCacheQ8:
 
     def evict_into(self, dst: "KVCacheQ8", budget: int, sink: int = 0, recent: int = 0,
                    kept: Optional[torch.Tensor] = None, max_len: int = 0) -> torch.Tensor:
-        """tg_cache_evict_q8: what stays of every sequence into dst; returns the kept slots [B, budget]."""
+        """tg_cache_evict_q8: what stays of every sequence into dst, whose lengths (a tensor of its own, or one that it shares
+        with other layers' targets) are written; returns the kept slots [B, budget]."""
         if kept is None:
             kept = torch.empty(self.batch, budget, dtype=torch.int32, device=self.handle.device)
         return tg.tg_cache_evict_q8(self.handle, dst.handle, kept, self._workspace, budget, sink=sink, recent=recent,

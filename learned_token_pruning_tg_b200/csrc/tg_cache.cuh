@@ -118,6 +118,12 @@ inline tg_status check_cache(const tg_cache_q8* c, Cache* out) {
     return TG_OK;
 }
 
+// Whether [p, p + bytes) and [q, q + more) share memory.
+inline bool overlap(const void* p, size_t bytes, const void* q, size_t more) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return p && q && x < y + more && y < x + bytes;
+}
+
 // Launch with programmatic dependent launch (every kernel calls pdl_wait() first).
 template <typename... P, typename... A>
 inline tg_status launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {

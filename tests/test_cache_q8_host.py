@@ -120,7 +120,7 @@ def test_append_refusals(lib):
 def test_decode_refusals(lib):
     vp = ctypes.c_void_p
 
-    def dec(c=None, q=16, n_q=1, Hq=4, tau=1.0, acc=0, max_len=0, out=16, ws=256, ws_bytes=1 << 30):
+    def dec(c=None, q=16, n_q=1, Hq=4, tau=1.0, acc=0, max_len=0, out=1 << 16, ws=256, ws_bytes=1 << 30):
         c = c or struct()
         return lib.tg_gated_decode_q8(ctypes.byref(c), vp(q), n_q, Hq, None, tau, acc, max_len, vp(out), None, vp(ws),
                                       ws_bytes, None)
@@ -129,6 +129,7 @@ def test_decode_refusals(lib):
     assert dec(n_q=0) == INV and dec(Hq=0) == INV and dec(Hq=5) == INV and dec(max_len=-1) == INV
     assert dec(tau=float("nan")) == INV and dec(tau=float("inf")) == INV
     assert dec(Hq=34) == UNS and dec(n_q=9) == UNS and dec(n_q=1 << 30) == UNS
+    assert dec(q=4096, out=4096) == INV and dec(q=4096, out=4096 + 1024) == INV    # the answer over the queries
     assert dec(q=0) == INV and dec(q=24) == INV and dec(out=8) == INV and dec(ws=0) == INV
     need = lib.tg_cache_workspace_bytes(ctypes.byref(struct()), 1, 4, 1)
     assert dec(acc=1, ws_bytes=need - 1) == INV

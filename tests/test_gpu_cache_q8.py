@@ -10,8 +10,8 @@ e = (d + 8) 2^-23 S, a weight by the factor exp(2 e) (its own and the sum's) plu
 rounding to fp16 (2^-12, ten times less common in the mean, counted whole) and the sums' fp32 (2^-20 for the lengths
 here).  Hence |out - want| <= (2 e + 2^-12 + 2^-19) sum_c p_c |v_c|, times 1 + 2^-8, and half a bf16 step of the
 result (2^-9 of its power of two, 2^-8 relative at most); |lse - want| <= e + 2^-20 + 2^-23 |lse|; a
-token's weight (2 e + 2^-18) of itself.  Weights under 2^-39 of the row's largest vanish in fp16's P: 2^-39 sum |v| is
-below 2^-19 of the result's bound for these lengths.
+token's weight (2 e + 2^-18) of itself.  (Weights below 2^-18 of the reference are rounded in steps of 2^-28 of it: 2^17 keys
+of such weights together would be 2^-12 off, the bound's own; these inputs leave few of them.)
 """
 import numpy as np
 import pytest
