@@ -10,8 +10,8 @@
 //   one token is a launch (3 us in a graph).
 // evict: one thread block, or a cluster of them, finds a sequence's kept slots by a radix select over the
 //   weights (11 + 11 + 10 bits of the order-preserving key), then one warp per new block gathers its 32 rows.
-//   Latency bounds both: 8961 tokens to 8704 (36 MB) 22.7 us, the select 10 of them; 65537 to 8704 26.6 us.
-//   (4 rows, or 1, a lane instead of 8: 24.1 and 24.8 us.)
+//   Latency bounds both: 8961 tokens to 8704 (36 MB) 20.5 us, 65537 to 8704 25 us, half of either the select.
+//   (4 rows, or 1, a lane instead of 8: 1.0 and 1.8 us more.)
 // read: HBM or L2 bounds it (24 MB of ragged sequences in about 6 us).
 #include "tg_cache.cuh"
 
@@ -212,6 +212,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kCluster = 8;              // thread blocks that select for one long sequence
 constexpr int kOneBlockKeys = 24 * 1024; // sequences up to this long: one thread block each
 constexpr int kMostKeys = 44 * 1024;     // keys that a thread block's shared memory holds
+constexpr int kFew = 256;                // keys that are ranked one by one instead of by two more passes
 
 struct EvictArgs {
     Cache src, dst;
@@ -220,6 +221,7 @@ struct EvictArgs {
     unsigned int* status;
     int64_t span;                        // keys that the launch expects of the longest sequence
     int room;                            // keys that its shared memory holds
+    int near;                            // whether most of a sequence is expected to stay
 };
 
 __device__ __forceinline__ void cluster_st(void* p, uint32_t rank, uint32_t v) {
@@ -269,10 +271,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
     __shared__ unsigned s_sum[CL > 1 ? 2048 : 1];   // (the next pass writes it behind a barrier of every reader)
     __shared__ unsigned s_scan[3][kSelWarps];
     __shared__ unsigned long long s_scan2[kSelWarps];
-    __shared__ unsigned s_pick[3][2], s_cnt[2];
+    __shared__ unsigned s_pick[3][3], s_cnt[2];
+    __shared__ __align__(16) uint32_t s_few[kFew];
+    __shared__ unsigned s_few_n, s_few_pick[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CL > 1 ? cluster_rank_in() : 0;
     for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0u;
+    if (tid == 0) s_few_n = 0u;
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.y, sink = static_cast<int>(a.sink), recent = static_cast<int>(a.recent);
@@ -280,19 +285,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
     // the keys of this block's part of a span as long as expected (inside the cache, whatever n turns out to be)
     const int expected = static_cast<int>((a.span + CL - 1) / CL);
     const float* w = a.src.w + b * a.src.capacity + sink;
-    {
-        const int64_t from = static_cast<int64_t>(rank) * expected, end = a.src.capacity - sink - from;
-        const int most = end < a.room ? static_cast<int>(end) : a.room;
-        for (int i0 = tid; i0 < most; i0 += 8 * kSelThreads) {
-            float x[8];
+    const int64_t from = static_cast<int64_t>(rank) * expected, end = a.src.capacity - sink - from;
+    const int most = end < a.room ? static_cast<int>(end) : a.room;
+    float x[8];
+    auto load = [&](int i0) {            // 8 keys a thread in one round trip
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i0 + kSelThreads * j < most) x[j] = __ldcg(w + from + i0 + kSelThreads * j);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i0 + kSelThreads * j < most) s_key[i0 + kSelThreads * j] = radix_key(x[j]);
-        }
-    }
+        for (int j = 0; j < 8; ++j)
+            if (i0 + kSelThreads * j < most) x[j] = __ldcg(w + from + i0 + kSelThreads * j);
+    };
+    load(tid);
     int32_t* kept = a.kept + b * a.budget;
     const int gtid = rank * kSelThreads + tid, gthreads = CL * kSelThreads;
     if (gtid == 0) a.dst.lengths[b] = static_cast<int32_t>(n < a.budget ? n : a.budget);
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
     const int c0 = static_cast<int>(min(static_cast<int64_t>(rank) * per, static_cast<int64_t>(m))), cn = min(per, m - c0);
     const int rounds = (per + 4 * kSelThreads - 1) / (4 * kSelThreads);
     const int w0 = min(warp * rounds * 128, cn), w1 = min(w0 + rounds * 128, cn);
-    w += c0;
     for (int i = gtid; i < sink; i += gthreads) kept[i] = i;
     for (int i = gtid; i < recent; i += gthreads) kept[budget - recent + i] = n - recent + i;
     if (kd == 0) return;
@@ -322,34 +322,56 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
                 if (i + q < end) k[q] = radix_key(__ldcg(w + i + q));
         }
     };
-    __syncthreads();                     // the histograms are zero, the keys there
+    // a thread's four keys into a histogram: one count where they agree (ties)
+    auto count4 = [&](unsigned* hist, const bool (&match)[4], const uint32_t (&digit)[4]) {
+        if (match[0] && match[1] && match[2] && match[3] && digit[0] == digit[1] && digit[0] == digit[2] &&
+            digit[0] == digit[3]) {
+            atomicAdd(&hist[digit[0]], 4u);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (match[q]) atomicAdd(&hist[digit[q]], 1u);
+        }
+    };
+    __syncthreads();                     // the histograms are zero
+    if (cached) {
+        // keys to shared memory, and the first pass's count as they come
+        for (int i0 = tid; i0 < most; i0 += 8 * kSelThreads) {
+            if (i0 != tid) load(i0);
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                bool match[4];
+                uint32_t digit[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = i0 + kSelThreads * (j + q);
+                    const uint32_t k = i < most ? radix_key(x[j + q]) : 0u;
+                    if (i < most) s_key[i] = k;
+                    match[q] = i < cn;
+                    digit[q] = k >> 21;
+                }
+                count4(s_hist[0], match, digit);
+            }
+        }
+    }
+    w += c0;
 
     uint32_t prefix = 0, pmask = 0;
     unsigned krem = static_cast<unsigned>(kd);   // rank of the threshold among the keys that match `prefix`
 #pragma unroll 1
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : (p == 1 ? 10 : 0), nb = p == 2 ? 1024 : 2048;
-        for (int i0 = 0; i0 < cn; i0 += 4 * kSelThreads) {
+        for (int i0 = 0; i0 < cn && !(p == 0 && cached); i0 += 4 * kSelThreads) {
             const int i = i0 + 4 * tid;
-            uint32_t k[4];
-            four(i, cn, k);
+            uint32_t k[4], digit[4];
             bool match[4];
-            uint32_t digit[4];
+            four(i, cn, k);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 match[q] = i + q < cn && (k[q] & pmask) == prefix;
                 digit[q] = (k[q] >> shift) & (nb - 1);
             }
-            // ties: one count for a thread's four keys
-            const bool same = match[0] && match[1] && match[2] && match[3] && digit[0] == digit[1] &&
-                              digit[0] == digit[2] && digit[0] == digit[3];
-            if (same) {
-                atomicAdd(&s_hist[p][digit[0]], 4u);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (match[q]) atomicAdd(&s_hist[p][digit[q]], 1u);
-            }
+            count4(s_hist[p], match, digit);
         }
         const unsigned* hist = s_hist[p];
         if constexpr (CL > 1) {
@@ -380,14 +402,52 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
         if (e < krem && krem <= e + h0) {
             s_pick[p][0] = d0;
             s_pick[p][1] = e;
+            s_pick[p][2] = h0;
         } else if (e + h0 < krem && krem <= e + h0 + h1) {
             s_pick[p][0] = d0 - 1;
             s_pick[p][1] = e + h0;
+            s_pick[p][2] = h1;
         }
         __syncthreads();
         prefix |= s_pick[p][0] << shift;
         pmask |= static_cast<uint32_t>(nb - 1) << shift;
         krem -= s_pick[p][1];
+        if (s_pick[p][2] == krem && prefix) {
+            // every key that matches stays: whatever is above prefix - 1
+            --prefix;
+            krem = 0;
+            break;
+        }
+        if (CL == 1 && p == 0 && s_pick[0][2] <= kFew) {
+            // few keys share the threshold's first digit: they are ranked against one another
+            for (int i0 = 0; i0 < cn; i0 += 4 * kSelThreads) {
+                const int i = i0 + 4 * tid;
+                uint32_t k[4];
+                four(i, cn, k);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < cn && (k[q] & pmask) == prefix) s_few[atomicAdd(&s_few_n, 1u)] = k[q];
+            }
+            __syncthreads();
+            const int few = static_cast<int>(s_few_n);
+            if (tid < few) {
+                const uint32_t k = s_few[tid];
+                unsigned above = 0, equal = 0;
+#pragma unroll 4
+                for (int i = 0; i < few; ++i) {
+                    above += s_few[i] > k;
+                    equal += s_few[i] == k;
+                }
+                if (above < krem && krem <= above + equal) {   // (every key equal to it says the same)
+                    s_few_pick[0] = k;
+                    s_few_pick[1] = krem - above;
+                }
+            }
+            __syncthreads();
+            prefix = s_few_pick[0];
+            krem = s_few_pick[1];
+            break;
+        }
     }
     // keys above the threshold `prefix` stay, and the first krem equal to it
     unsigned gt = 0, eq = 0;
@@ -452,11 +512,20 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_evict_gather_kernel(cons
     constexpr int LPR = D / 16;          // lanes of a row of codes
     constexpr int RPL = 32 / LPR;
     constexpr int N = kBlock / RPL;
-    pdl_wait();
-    pdl_trigger();
     const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int Hkv = a.src.Hkv, head = unit % Hkv, is_v = unit / Hkv % 2;
     const int64_t j = unit / (2 * Hkv), b = blockIdx.y;
+    if (a.near && j * kBlock < a.budget) {
+        // While the select still runs (it began when all that wrote src had ended): this block's share of a sequence
+        // of which most will stay, into L2.
+        const int64_t n = min(max(static_cast<int64_t>(__ldg(a.src.lengths + b)), static_cast<int64_t>(0)), a.src.capacity);
+        const int64_t r0 = j * kBlock * n / a.budget, r1 = min((j + 1) * kBlock * n / a.budget, n);
+        const uint8_t* p = (is_v ? a.src.v : a.src.k) + b * a.src.ld_seq + head * D;
+        for (int64_t r = r0 + lane; r < r1; r += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + r * a.src.ld_token));
+    }
+    pdl_wait();
+    pdl_trigger();
     if (j * kBlock >= a.budget) return;
     const int slot = j * kBlock + lane < a.budget ? a.kept[b * a.budget + j * kBlock + lane] : -1;
     if (!__any_sync(0xffffffffu, slot >= 0)) return;
@@ -658,6 +727,7 @@ extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8
     if (max_len == 0 || max_len > src->capacity) max_len = src->capacity;
     cudaStream_t st = as_stream(stream);
     tg_status r;
+    a.near = max_len <= 2 * budget;
     const int64_t keys = max_len - sink - recent;
     r = keys <= q8::kOneBlockKeys ? q8::launch_select<1>(a, keys, st) : q8::launch_select<q8::kCluster>(a, keys, st);
     if (r != TG_OK || budget == 0) return r;

@@ -610,6 +610,8 @@ def test_strided_cache():
     ([1], 1, 0, 1, 1, 64, "random"),
     ([96, 95], 95, 3, 5, 2, 64, "constant"),                # one token leaves
     ([3000, 2999], 1000, 4, 64, 1, 64, "random"),
+    ([3000], 1000, 4, 64, 1, 64, "close"),                  # one first digit for all: every pass has to look
+    ([3000], 1000, 4, 64, 1, 64, "two"),                    # two values, the budget between them
 ])
 def test_evict(fmt, lens, budget, sink, recent, H, d, wts):
     B, cap = len(lens), (max(lens) + 31) // 32 * 32
@@ -618,6 +620,10 @@ def test_evict(fmt, lens, budget, sink, recent, H, d, wts):
         w = torch.randint(0, 4, (B, cap), generator=g).float()
     elif wts == "constant":
         w.fill_(0.25)
+    elif wts == "close":
+        w = 1.0 + torch.rand(B, cap, generator=g) * 2.0 ** -8
+    elif wts == "two":
+        w = torch.where(torch.arange(cap) % 3 == 0, 1.0, 0.5).expand(B, cap).contiguous()
     elif wts == "special":
         w = torch.randn(B, cap, generator=g)
         for i, x in enumerate((float("nan"), float("inf"), float("-inf"), 0.0, -0.0)):
@@ -651,7 +657,8 @@ def test_evict(fmt, lens, budget, sink, recent, H, d, wts):
             assert np.array_equal(getattr(dst, m + "_scale")[b: b + 1].double().cpu().numpy(), scale, equal_nan=True)
 
 
-@pytest.mark.parametrize("T,budget,max_len", [(70001, 8704, 0), (70001, 8704, 1000), (450000, 20000, 0)])
+@pytest.mark.parametrize("T,budget,max_len", [(70001, 8704, 0), (70001, 8704, 1000), (450000, 20000, 0),
+                                              (24000, 23000, 0), (30000, 29000, 0), (30000, 600, 0)])
 def test_evict_long(T, budget, max_len):
     """Long sequences (keys in shared memory, or read again where they do not fit it or max_len was too small)."""
     g = torch.Generator(device="cuda").manual_seed(T)
