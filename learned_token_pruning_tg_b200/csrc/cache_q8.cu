@@ -6,7 +6,7 @@
 //
 // append: bf16 rows (2 rows a warp load, 16 bytes a lane) -> codes (8 bytes a lane).  A block with tokens of an
 //   earlier append keeps the larger scale; its codes move to it by one multiplication with a power
-//   of two and one rounding.  HBM bounds a prompt: 65536 tokens of 8 heads of 128 (403 MB) take 67.5 us, 6.0 TB/s;
+//   of two and one rounding.  HBM bounds a prompt: 65536 tokens of 8 heads of 128 (403 MB) take 63.3 us, 6.4 TB/s;
 //   one token is a launch (3 us in a graph).
 // evict: one thread block, or a cluster of them, finds a sequence's kept slots by a radix select over the
 //   weights (11 + 11 + 10 bits of the order-preserving key), then one warp per new block gathers its 32 rows.
@@ -18,7 +18,8 @@
 namespace tg {
 namespace q8 {
 
-constexpr int kWarps = 8;                // warps of an append, read or gather thread block
+constexpr int kWarps = 4;                // warps of an append or gather thread block (8: 67.5 us for the prompt below)
+constexpr int kReadThreads = 256;
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -176,7 +177,7 @@ struct ReadArgs {
 // block takes `tokens` tokens (about one item a thread: many small thread blocks cover the latency best, 32 tokens a
 // thread block took 1.6 times as long for 16 ragged sequences of up to 840).
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const ReadArgs a) {
     pdl_wait();
     pdl_trigger();
     const int64_t b = blockIdx.y, row0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_q8_kernel(const ReadAr
     if (rows > a.n) rows = a.n;          // (first + n <= capacity)
     rows = rows - row0 < a.tokens ? rows - row0 : a.tokens;
     const int per_row = a.c.Hkv * (D / 8), items = static_cast<int>(rows) * per_row;
-    for (int i = threadIdx.x; i < items; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < items; i += kReadThreads) {
         const int r = i / per_row, col = (i - r * per_row) * 8;
         const int64_t slot = a.first + row0 + r;
         const int64_t from = b * a.c.ld_seq + slot * a.c.ld_token + col;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) cache_evict_select_kernel(cons
 
 // One warp: one new block of one head, K or V.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32, 4) cache_evict_gather_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const EvictArgs a) {
     constexpr int LPR = D / 16;          // lanes of a row of codes
     constexpr int RPL = 32 / LPR;
     constexpr int N = kBlock / RPL;
@@ -683,13 +684,13 @@ extern "C" tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, i
     a.k = reinterpret_cast<__nv_bfloat16*>(k_out);
     a.v = reinterpret_cast<__nv_bfloat16*>(v_out);
     const int per_row = a.c.Hkv * (cache->d_h / 8);
-    a.tokens = per_row < q8::kWarps * 32 ? q8::kWarps * 32 / per_row : 1;
+    a.tokens = per_row < q8::kReadThreads ? q8::kReadThreads / per_row : 1;
     const dim3 grid(static_cast<unsigned>((n + a.tokens - 1) / a.tokens), static_cast<unsigned>(a.c.batch));
     auto kern = cache->d_h == 128 ? (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<128, TG_CACHE_E4M3>
                                                                     : q8::cache_read_q8_kernel<128, TG_CACHE_INT8>)
                                   : (cache->format == TG_CACHE_E4M3 ? q8::cache_read_q8_kernel<64, TG_CACHE_E4M3>
                                                                     : q8::cache_read_q8_kernel<64, TG_CACHE_INT8>);
-    return q8::launch_pdl(kern, grid, dim3(q8::kWarps * 32), 0, as_stream(stream), a);
+    return q8::launch_pdl(kern, grid, dim3(q8::kReadThreads), 0, as_stream(stream), a);
 }
 
 extern "C" tg_status tg_cache_evict_q8(const tg_cache_q8* src, const tg_cache_q8* dst, int64_t budget, int64_t sink,

@@ -852,11 +852,19 @@ __device__ __forceinline__ void add_tiles(const DecodeArgs& a, WeightRoom& room,
 // w[b, c] += sum over heads and rows of 2^(x - lse2), thread block x of nx: 64 keys and 4 groups of heads, up to 4 tiles
 // of keys at once so that many loads are under way, the groups' sums in a fixed order.  The log-sum-exps come from
 // the parts themselves, so that this does not wait for their merging.
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& room, int b, int x, int nx) {
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& room, int b, int x, int nx, bool done) {
     const int tid = threadIdx.x, Hkv = a.c.Hkv, len = length_of(a.c, b, a.status);
     if (static_cast<int64_t>(x) * kWeightKeys >= len) return;
-    // 8 lanes a row
-    for (int i = tid / 8; i < (Hkv * a.Rp + 3) / 4 * 4; i += kFinThreads / 8) {
+    if (done) {
+        // every head's rows are finished already
+        for (int i = tid; i < Hkv * a.Rp; i += kFinThreads) {
+            const int h = i / a.Rp, r = i - h * a.Rp;
+            const float v = r < a.R ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : -INFINITY;
+            room.lse[i] = v == -INFINITY ? INFINITY : v;
+        }
+    }
+    // else 8 lanes a row
+    for (int i = tid / 8; !done && i < (Hkv * a.Rp + 3) / 4 * 4; i += kFinThreads / 8) {
         const int h = i / a.Rp, r = i % a.Rp;
         const bool row = h < Hkv && r < a.R;
         const int2 hd = row ? a.heads[b * Hkv + h] : make_int2(0, 0);
@@ -908,7 +916,7 @@ __global__ void __launch_bounds__(kFinThreads, 4) decode_q8_finish_kernel(const 
     if (x < merges)
         merge_parts<D>(a, room.merge, b, x / chunks, x % chunks * kRows);
     else
-        add_weights(a, room.weights, b, x - merges, gridDim.x - merges);
+        add_weights(a, room.weights, b, x - merges, gridDim.x - merges, merges == 0);
 }
 
 // Workspace: status header, heads, lse2, parts, logits (each from a 256-byte boundary).
