@@ -495,8 +495,9 @@ tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, t
  * Hq] fp32 or NULL.  The bias is 0 where cache->s or gain is NULL.
  * max_len: an upper bound on lengths that sizes the launch (0 = capacity);
  * a longer sequence is still read whole, by fewer thread blocks.
- * Supported: Hq a multiple of Hkv, n_q * Hq / Hkv <= 16, tau finite.  One launch,
- * a second one with accumulate.  Every code is read once (HBM-bound); logits, softmax
+ * Supported: Hq a multiple of Hkv, n_q * Hq / Hkv <= 16, tau finite.  One launch;
+ * a second one for long caches, which several thread blocks share a head of, and with
+ * accumulate.  Every code is read once (HBM-bound); logits, softmax
  * and sums in fp32, the products on the tensor cores from the codes in fp16
  * (exact) with q scaled by a power of two to fp16 and the softmax's weights
  * rounded to fp16.  Deterministic. */

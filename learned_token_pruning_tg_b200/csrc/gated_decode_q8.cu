@@ -35,7 +35,7 @@
 // Measured (one B200, 8 KV heads of 128, 2 query heads each): 65537 keys 32.1 us, 4.2 TB/s of the 6.55 a copy reaches;
 // about 10 us of every long step are fixed (launch and lengths 2.5, first loads 1.5, the last unit and the merge 2.5,
 // the second kernel 3.7), the loads alone run at 5.8 TB/s, and the arithmetic without them takes half their time.  Two
-// sequences of 131073 keys 92.6 us, 5.8 TB/s.  8705 keys 11.7 us (a cluster of 8 a head), 15.2 us with the weights.
+// sequences of 131073 keys 93 us, 5.8 TB/s.  8705 keys 11.8 us (a cluster of 8 a head), 15.1 us with the weights.
 #include <cmath>
 
 #include "tg_cache.cuh"
