@@ -35,7 +35,7 @@
 // Measured (one B200, 8 KV heads of 128, 2 query heads each): 65537 keys 32.1 us, 4.2 TB/s of the 6.55 a copy reaches;
 // about 10 us of every long step are fixed (launch and lengths 2.5, first loads 1.5, the last unit and the merge 2.5,
 // the second kernel 3.7), the loads alone run at 5.8 TB/s, and the arithmetic without them takes half their time.  Two
-// sequences of 131073 keys 93 us, 5.8 TB/s.  8705 keys 11.8 us (a cluster of 8 a head), 15.1 us with the weights.
+// sequences of 131073 keys 93 us, 5.8 TB/s.  8705 keys 11.8 us (a cluster a head), 15.1 us with the weights.
 #include <cmath>
 
 #include "tg_cache.cuh"
@@ -460,7 +460,7 @@ struct Shared {
     unsigned red[kW], base, next, total;
     int n_seg, b;
     // what the thread blocks of a cluster hand to the one that finishes a number: their sums and references
-    float4 sums[8 * NT * D / 4];
+    float4 sums[8 * NT * D / 4 + kMaxCluster];
     float2 ml[kMaxCluster][8 * NT];
 };
 
@@ -522,7 +522,7 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& 
             add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), f);
         }
         if (a.cluster > 1) {
-            const int v = r * (D / 4) + d / 4, rank = cluster_rank_in(), each = a.R * (D / 4) / a.cluster;
+            const int v = r * (D / 4) + d / 4, rank = cluster_rank_in(), each = (a.R * (D / 4) - 1) / a.cluster + 1;
             store_cluster(&sh.sums[rank * each + v / a.cluster], v % a.cluster, o);
             if (d / 4 < a.cluster) store_cluster(&sh.ml[rank][r], d / 4, make_float2(m, l));
         } else if (sg.parts == 1) {
@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
         if (a.cluster > 1) {
             __syncwarp();
             cluster_sync_all();
-            const int each = a.R * (D / 4) / a.cluster;
-            for (int i = tid; i < each; i += kThreads) {
+            const int vecs = a.R * (D / 4), each = (vecs - 1) / a.cluster + 1;
+            for (int i = tid; i * a.cluster + rank < vecs; i += kThreads) {
                 const int v = i * a.cluster + rank, r = v / (D / 4), d = v % (D / 4) * 4;
                 float m = kNothing, l = 0.0f;
                 for (int p = 0; p < a.cluster; ++p) m = fmaxf(m, sh.ml[p][r].x);
@@ -939,9 +939,9 @@ static Layout layout(const Cache& c, int d_h, int R, bool weights) {
 // Clusters of `cl` thread blocks that run at the same time (0: none fits), asked for once per kernel and device.
 template <int D, int FMT, int NT, bool kWeights>
 static int max_clusters(int cl) {
-    static std::atomic<int> cache[64][5];
-    const int dev = current_device(), k = cl == 1 ? 0 : cl == 2 ? 1 : cl == 4 ? 2 : cl == 8 ? 3 : 4;
-    if (dev >= 0 && cache[dev][k].load(std::memory_order_acquire)) return cache[dev][k].load() - 1;
+    static std::atomic<int> cache[64][kMaxCluster + 1];
+    const int dev = current_device();
+    if (dev >= 0 && cache[dev][cl].load(std::memory_order_acquire)) return cache[dev][cl].load() - 1;
     auto kern = gated_decode_q8_kernel<D, FMT, NT, kWeights>;
     constexpr int kSmem = static_cast<int>(sizeof(Shared<D, NT>));
     int n = 0;
@@ -964,24 +964,31 @@ static int max_clusters(int cl) {
     } else {
         cudaGetLastError();
     }
-    if (dev >= 0) cache[dev][k].store(n + 1, std::memory_order_release);
+    if (dev >= 0) cache[dev][cl].store(n + 1, std::memory_order_release);
     return n;
 }
 
-// Thread blocks of a head: as many as give every warp one unit, or the most whose clusters all run at the same time;
-// 0 (runs of units) where a warp would have more than 2 units in a thread block alone, or 4 in a cluster.  Returns -1
-// where the kernel cannot be set up.  Measured, cluster against runs, in us: 8 heads of 2 rows, 1025 keys 8.0 (4) to
-// 9.7, 8705 keys 11.5 (8) to 13.1, 12289 keys 14.5 (8) to 14.1; one head of 8 rows, 8705 keys 10.0 (16) to 15.1;
-// 16 heads of 2 rows, 4097 keys 11.5 (4) to 13.3, 12289 keys 22.3 (4) to 20.8.
+// Thread blocks of a head: the fewest that give a warp no more units than the most whose clusters all run at the same
+// time would, one unit where that many fit; 0 (runs of units) where a warp would have more than 2 units in a thread
+// block alone, or 4 in a cluster.  Returns -1 where the kernel cannot be set up.  Measured, cluster against runs, in
+// us: 8 heads of 2 rows, 1025 keys 8.0 (3) to 9.7, 8705 keys 11.5 to 13.1, 12289 keys 13.2 to 14.1; one head of 8 rows,
+// 8705 keys 9.9 (12) to 15.1; 16 heads of 2 rows, 4097 keys 10.2 to 13.3, 8705 keys 13.8 to 16.6.  Sizes that are powers
+// of two alone: 16 heads, 2049 keys 9.7 to 7.9, 8705 keys 16.6 to 13.8; 8 heads as they are.
 template <int D, int FMT, int NT, bool kWeights>
 static int cluster_for(int64_t heads, int64_t blocks) {
     static std::atomic<int> smem_set[64];
     if (!set_max_dynamic_smem(gated_decode_q8_kernel<D, FMT, NT, kWeights>, static_cast<int>(sizeof(Shared<D, NT>)), smem_set))
         return -1;
-    int best = 1;
-    for (int cl = 2; cl <= kMaxCluster && blocks > warps_of(NT) * best; cl *= 2)
-        if (heads * cl <= num_sms() && heads <= max_clusters<D, FMT, NT, kWeights>(cl)) best = cl;
-    return blocks <= (best == 1 ? 2 : 4) * warps_of(NT) * best ? best : 0;
+    constexpr int W = warps_of(NT);
+    if (blocks <= W) return 1;
+    int64_t cl = (blocks + W - 1) / W;
+    if (cl > kMaxCluster) cl = kMaxCluster;
+    if (cl > num_sms() / heads) cl = num_sms() / heads;
+    while (cl > 1 && heads > max_clusters<D, FMT, NT, kWeights>(static_cast<int>(cl))) --cl;
+    if (cl < 1) cl = 1;
+    const int64_t units = (blocks + W * cl - 1) / (W * cl);  // of a warp
+    if (units > (cl == 1 ? 2 : 4)) return 0;
+    return static_cast<int>((blocks + W * units - 1) / (W * units));
 }
 
 template <int D, int FMT, int NT, bool kWeights>

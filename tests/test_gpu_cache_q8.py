@@ -334,11 +334,20 @@ def test_decode_ragged_runs(fmt, B, most, Hq, Hkv, d, n_q):
 
 @pytest.mark.parametrize("max_len", [1, 400, 800, 1600, 3100, 6200, 0])
 def test_decode_any_launch(max_len):
-    """One, 2, 4, 8 or 16 thread blocks a head, or runs: every launch reads the same caches whole."""
+    """One thread block a head, a cluster of them, or runs: every launch reads the same caches whole."""
     lens = [13000, 0, 77]
     cache, check, nums, s, w, g = random_cache("e4m3", 3, 13024, 1, 64, lens, seed=21)
     q = torch.randn(3, 2, 3, 64, generator=g).to(torch.bfloat16)
     check_decode(cache, check, nums, s, w, q, 2 * torch.rand(3, generator=g), 1.1, lens, max_len=max_len)
+
+
+@pytest.mark.parametrize("Hq,d", [(3, 64), (5, 128), (15, 64)])
+@pytest.mark.parametrize("T", [800, 1700, 2600, 3500, 4900, 6100])
+def test_decode_any_cluster(T, Hq, d):
+    """One KV head whose units go to 3 to 16 thread blocks, with rows that they do not share evenly."""
+    cache, check, nums, s, w, g = random_cache("e4m3", 1, 6112, 1, d, [T], seed=T)
+    q = torch.randn(1, 1, Hq, d, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, torch.rand(Hq, generator=g) * 2, 1.5, [T], max_len=T)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
