@@ -463,6 +463,49 @@ def test_decode_long(fmt, T, Hq, Hkv, n_q):
     assert torch.equal(again.view(torch.int16), out.view(torch.int16))
 
 
+def test_offsets_past_32_bits():
+    """The end of the second of two sequences of 2.2 million tokens, 4.5 GB into the codes, against a small cache with the
+    same tokens at the same place of their blocks."""
+    B, H, d, cap, n, new_ = 2, 8, 128, 2_200_000, 2_199_990, 70
+    at = (n - new_) % 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(3, B, new_, H, d, generator=g, device="cuda").to(torch.bfloat16)
+    bias = 0.6 * torch.randn(B, new_, generator=g, device="cuda")
+    gain = 0.5 + torch.rand(2 * H, generator=g, device="cuda")
+    q = torch.randn(B, 1, 2 * H, d, generator=g, device="cuda").to(torch.bfloat16)
+    got = []
+    for size, length in ((cap, n), (96, at + new_)):
+        cache = KVCacheQ8(B, size, H, d)
+        cache.k_scale.fill_(1.0)
+        cache.v_scale.fill_(1.0)
+        cache.s.fill_(float("-inf"))
+        cache.lengths.copy_(ints([at + new_, length]))
+        cache.append(x[0], x[1], bias)
+        k, v = torch.empty_like(x[0]), torch.empty_like(x[1])
+        cache.read(k, v, first=length - new_)
+        lse = torch.empty(B, 1, 2 * H, device="cuda")
+        out = cache.decode(q, gain=gain, tau=1.2, lse=lse, accumulate=True)
+        dst = KVCacheQ8(B, new_, H, d)
+        kept = cache.evict_into(dst, new_, recent=new_)
+        assert torch.equal(kept[1], torch.arange(length - new_, length, dtype=torch.int32, device="cuda"))
+        assert cache.device_status() == 0
+        got.append((cache, k[1], v[1], out, lse, dst, cache.w[1, length - new_ : length].clone()))
+    (_, k, v, out, lse, dst, w), (small, k2, v2, _, _, dst2, _) = got
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    for t, t2 in ((dst.k, dst2.k), (dst.v, dst2.v)):
+        assert torch.equal(t[1, :new_].view(torch.uint8), t2[1, :new_].view(torch.uint8))
+    assert torch.equal(dst.k_scale, dst2.k_scale) and torch.equal(dst.v_scale, dst2.v_scale)
+    # the bounds of test_decode_long
+    want, want_lse, want_w, mass, size = decode_in_torch(small, q, gain, 1.2, at + new_)
+    e = (d + 8) * 2.0 ** -23 * (size + 4 * 0.6 * 5)
+    err = (out.double() - want).abs()
+    step = torch.exp2(torch.floor(torch.log2(want.abs() + 2.0 ** -10 * mass)) - 8)
+    assert bool((err <= (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + step).all())
+    assert float((lse.double() - want_lse).abs().max()) <= e + 2.0 ** -20 + 2.0 ** -23 * float(want_lse.abs().max())
+    dw = (w.double() - want_w[1, at:]).abs()
+    assert bool((dw <= (2 * e + 2.0 ** -18 + 2.0 ** -22) * want_w[1, at:]).all())
+
+
 # ------------------------------------------------------------------------------------------- a step, captured
 def test_steps_in_a_graph_and_on_streams():
     """Append and decode captured once and replayed while the sequences grow: the same bits as the calls made one by
