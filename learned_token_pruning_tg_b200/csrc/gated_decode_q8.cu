@@ -25,7 +25,10 @@
 // take 128 keys a step and bring the 8 columns back through TMEM; the products are far from the bound.)
 //
 // A row's reference m moves only when a logit exceeds it by more than 2^kLazy, and V's scales are folded into the
-// weights relative to a reference of their own, so the V product adds to the output in the MMA itself.
+// weights relative to a reference of their own, so the V product adds to the output in the MMA itself.  V's reference is
+// a power of two and only rises (to a scale more than kRatio times as large), so the output in its units stays below 2^55:
+// weights of 2^15, codes of 2^9, 2^31 keys.  A unit whose scale is more than kRatio times smaller, or all zeros, gets a
+// product of its own that is added in fp32.
 //
 // Roundings: q is scaled to fp16 by a power of two per row (bf16 has fewer bits: only
 // elements 2^-25 of the row's largest are lost); the weights 2^(x - m + 8) vscale / vref are rounded to fp16
@@ -53,8 +56,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 8.0f;           // weights are 2^(x - m + kShift) ...
 constexpr float kLazy = 3.0f;            // ... at most 2^(kShift + kLazy) ...
-constexpr float kRatio = 16.0f;          // ... times vscale / vref, within 1 / kRatio .. kRatio
-constexpr float kMostUp = 18446744073709551616.0f;   // 2^64
+constexpr float kRatio = 16.0f;          // ... times vscale / vref, at most kRatio, and not below 1 / kRatio in a joint product
 constexpr float kNothing = -3.402823466e38f;   // the reference before the first logit
 constexpr int kFinThreads = 256, kWeightKeys = 64, kWeightGroups = kFinThreads / kWeightKeys;
 constexpr int kWeightTiles = kWeightGroups;   // tiles of keys at a time, one for each group to finish
@@ -138,7 +140,7 @@ struct Warp {
     uint32_t qf[D / 16][NT][2];
     float f[NT][2], gl2[NT][2];          // logit factor and gain of this lane's query rows 8 nt + 2 t + {0, 1}
     float m[NT][2], l[NT][2], o[D / 16][NT][4];   // m: the reference less kShift
-    float vref;                          // o is in units of it
+    float vinv;                          // o is in units of vref, a power of two; this is its inverse
 
     __device__ __forceinline__ explicit Warp(const DecodeArgs& args)
         : a(args), lane(threadIdx.x & 31), g(lane >> 2), t(lane & 3) {}
@@ -208,7 +210,7 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[dm][nt][i] = 0.0f;
-        vref = 0.0f;
+        vinv = inverse(__int_as_float(1 << 23));   // the least scale
     }
 
     __device__ __forceinline__ void load_keys(KeyRegs<D>& k, const uint8_t* p, const float* scale, const float* s) const {
@@ -231,9 +233,15 @@ struct Warp {
         v.scale = __ldg(scale);
     }
 
-    // Weights of a unit as B operands, times V's scale over its reference; the sums.
+    // 1 / x for a power of two x in 2^-126 .. 2^126
+    __device__ __forceinline__ static float inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
+
+    // Whether a unit's product is added on its own: V's scale is far below the reference.
+    __device__ __forceinline__ static bool apart(float ratio) { return ratio < 1.0f / kRatio; }
+
+    // Weights of a unit as B operands, times V's scale over its reference (ratio; not where that is apart); the sums.
     __device__ __forceinline__ void scores(const KeyRegs<D>& k, float v_scale, int b, int kvh, int blk, int len,
-                                           uint32_t (&pf)[2][NT][2]) {
+                                           uint32_t (&pf)[2][NT][2], float& ratio) {
         float x[2][NT][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -318,20 +326,21 @@ struct Warp {
                     }
                 }
         }
-        float ratio = __fdividef(v_scale, vref);
-        if (!(ratio <= kRatio && ratio >= 1.0f / kRatio)) {
-            // far from V's reference, or the first: it moves to this scale, down by 2^64 at most (o is below 2^55:
-            // weights of 2^15, codes of 2^9, 2^31 keys; further down the weights carry the rest)
-            const float move = fminf(__fdividef(vref, v_scale), kMostUp);
+        ratio = v_scale * vinv;
+        if (!(ratio <= kRatio)) {
+            // far above V's reference: it rises to this scale's power of two (what is 2^149 below vanishes)
+            const float up = inverse(__int_as_float(min(__float_as_int(v_scale) >> 23, 253) << 23));
+            const float move = inverse(vinv) * up;
+            vinv = up;
 #pragma unroll
             for (int dm = 0; dm < D / 16; ++dm)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[dm][nt][c] *= move;
-            vref = fmaxf(v_scale, vref * (1.0f / kMostUp));
-            ratio = __fdividef(v_scale, vref);
+            ratio = v_scale * vinv;
         }
+        const float f = apart(ratio) ? 1.0f : ratio;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -342,8 +351,8 @@ struct Warp {
                     p[c] = ex2(x[i][nt][c] - m[nt][c & 1]);
                     l[nt][c & 1] += p[c];
                 }
-                pf[i][nt][0] = transpose8x8(pack_f16x2(p[0] * ratio, p[1] * ratio));
-                pf[i][nt][1] = transpose8x8(pack_f16x2(p[2] * ratio, p[3] * ratio));
+                pf[i][nt][0] = transpose8x8(pack_f16x2(p[0] * f, p[1] * f));
+                pf[i][nt][1] = transpose8x8(pack_f16x2(p[2] * f, p[3] * f));
             }
     }
 
@@ -361,7 +370,8 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt) mma(acc[nt], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
         }
     }
-    __device__ __forceinline__ void values(ValueRegs<D>& v, int blk, int len, const uint32_t (&pf)[2][NT][2]) {
+    __device__ __forceinline__ void values(ValueRegs<D>& v, int blk, int len, const uint32_t (&pf)[2][NT][2],
+                                           float ratio) {
         if (FMT == TG_CACHE_E4M3 && (blk + 1) * kBlock > len) {
             // rows behind the sequence may hold anything, NaN codes too: their weight is 0
 #pragma unroll
@@ -372,8 +382,20 @@ struct Warp {
 #pragma unroll
                         for (int w = 0; w < D / 32; ++w) v.w[i][j][w] = 0u;
         }
+        if (apart(ratio)) {
 #pragma unroll
-        for (int dm = 0; dm < D / 16; ++dm) product(v, dm, pf, o[dm]);
+            for (int dm = 0; dm < D / 16; ++dm) {
+                float acc[NT][4] = {};
+                product(v, dm, pf, acc);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[dm][nt][c] = fmaf(acc[nt][c], ratio, o[dm][nt][c]);
+            }
+        } else {
+#pragma unroll
+            for (int dm = 0; dm < D / 16; ++dm) product(v, dm, pf, o[dm]);
+        }
     }
 
     // Units u0, u0 + step, ... < u1 of one head.
@@ -393,14 +415,15 @@ struct Warp {
         begin(b, kvh);
         for (int u = u0; u < u1; u += step) {
             uint32_t pf[2][NT][2];
-            scores(k, v.scale, b, kvh, u, len, pf);
+            float ratio;
+            scores(k, v.scale, b, kvh, u, len, pf, ratio);
             pk += step * block_codes;
             pv += step * block_codes;
             ks += step * a.c.Hkv;
             vs += step * a.c.Hkv;
             s += step * kBlock;
             if (u + step < u1) load_keys(k, pk, ks, s);
-            values(v, u, len, pf);
+            values(v, u, len, pf, ratio);
             if (u + step < u1) load_values(v, pv, vs);
         }
 #pragma unroll
@@ -467,6 +490,7 @@ struct Shared {
 template <int D, int FMT, int NT, bool kWeights>
 __device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh,
                                           const Warp<D, FMT, NT, kWeights>& wp, int entry) {
+    const float vref = wp.inverse(wp.vinv);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -481,7 +505,7 @@ __device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh
 #pragma unroll
                 for (int dm = 0; dm < D / 16; ++dm)
                     *reinterpret_cast<float2*>(to + 2 * dm) =
-                        make_float2(wp.o[dm][nt][c] * wp.vref, wp.o[dm][nt][2 + c] * wp.vref);
+                        make_float2(wp.o[dm][nt][c] * vref, wp.o[dm][nt][2 + c] * vref);
             }
         }
 }

@@ -1,0 +1,92 @@
+"""The 8-bit cache's kernels over the whole range of scales and biases, against the 64-bit reference (tests/cache_ref.py).
+
+The bounds are those that tests/test_gpu_cache_q8.py derives; where a test needs another, it says why.
+"""
+import numpy as np
+import pytest
+import torch
+
+from learned_token_pruning_tg_b200.cache import KVCacheQ8
+from tests import cache_ref as ref
+from tests.test_gpu_cache_q8 import FORMATS, check_decode, half_step, random_cache
+
+pytestmark = pytest.mark.gpu
+
+# A block of a sequence in one thread block of 12 warps is a warp's every twelfth one, in a cluster of 16 every 192nd; in
+# runs a warp's blocks follow one another.  (B, tokens, max_len, blocks that share an entry of a pattern)
+LAUNCHES = {"one thread block": (1, 32 * 72 - 5, 1, 12), "cluster": (1, 32 * 768 - 5, 0, 192), "runs": (160, 32 * 40 - 5, 0, 1)}
+ZERO = None                              # a block of zeros, under the least scale, as an append leaves it
+
+
+def scaled_values(cache, nums, exponents, lens, fmt):
+    """V's blocks under 2^exponents[j] (ZERO: zeros under 2^-126) instead of their own scales."""
+    B, cap, H, d = cache.v.shape
+    codes, scale = cache.v.clone(), torch.full((B, cap // 32, H), float("nan"))
+    for j, e in enumerate(exponents):
+        if e is ZERO:
+            codes[:, 32 * j: 32 * j + 32] = 0
+        scale[:, j] = 2.0 ** (-126 if e is ZERO else e)
+    for b in range(B):
+        codes.view(torch.uint8)[b, lens[b]:] = 0x7f
+    cache.v.copy_(codes)
+    cache.v_scale.copy_(scale)
+    nums["v"] = ref.values(np.nan_to_num(ref.code_values(codes)), np.nan_to_num(scale.double().numpy()))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("pattern", [
+    (-6, ZERO, ZERO, -6, ZERO, -6), (-6, -6, ZERO, ZERO, ZERO, ZERO), (ZERO, ZERO, -6, ZERO, ZERO, ZERO),
+    (0, -40, -80, -100, -20, 3), (-100, -60, -20, 20, 60, 90), (60, -60, 60, -60, 0, -60), (0, -4, -8, -12, -16, -40),
+], ids=str)
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_decode_values_of_far_scales(fmt, pattern, launch):
+    """Blocks of V whose scales lie far apart, and blocks of zeros, one after the other in a warp."""
+    B, T, max_len, every = LAUNCHES[launch]
+    lens = [T - 32 * (b % 3) for b in range(B)]
+    cache, check, nums, s, w, g = random_cache(fmt, B, T + 5, 1, 64, lens, seed=len(launch))
+    scaled_values(cache, nums, [pattern[j // every % 6] for j in range((T + 5) // 32)], lens, fmt)
+    q = torch.randn(B, 1, 3, 64, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, 2 * torch.rand(3, generator=g), 1.2, lens, max_len=max_len)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_decode_small_values_behind_masked_large_ones(fmt, launch):
+    """The blocks of the largest scale are masked by a bias of -inf: the answer is the small ones'."""
+    B, T, max_len, every = LAUNCHES[launch]
+    lens = [T] * B
+    cache, check, nums, s, w, g = random_cache(fmt, B, T + 5, 2, 64, lens, seed=3)
+    exponents = [(0, -100, -90)[j // every % 3] for j in range((T + 5) // 32)]
+    scaled_values(cache, nums, exponents, lens, fmt)
+    mask = torch.tensor([e == 0 for e in exponents]).repeat_interleave(32)[:T]
+    s[:, :T] = torch.where(mask, float("-inf"), s[:, :T])
+    cache.s.copy_(s)
+    q = torch.randn(B, 1, 4, 64, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, torch.full((4,), 1.25), 1.2, lens, max_len=max_len)
+
+
+def test_decode_over_appended_zeros():
+    """A prompt whose middle is padding of zero rows, as the append itself lays it out, without and with the padding masked."""
+    B, T, H, d = 1, 200000, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(8)
+    cache = KVCacheQ8(B, T, H, d)
+    cache.lengths.fill_(T)
+    x = torch.randn(2, B, T, H, d, generator=g, device="cuda").to(torch.bfloat16)
+    x[:, :, 3000:3400] = 0
+    x[1, :, 20000:20100, 1] = 0
+    q = torch.randn(B, 1, 4, d, generator=g, device="cuda").to(torch.bfloat16)
+    gain = torch.ones(4, device="cuda")
+    s = torch.zeros(B, T, device="cuda")
+    for masked in (False, True):
+        if masked:
+            s[:, 3000:3400] = float("-inf")
+        cache.append(x[0], x[1], s=s)
+        out = cache.decode(q, gain=gain)
+        assert cache.device_status() == 0
+        k, v = (ref.values(ref.code_values(c), sc.double().cpu().numpy()) for c, sc in
+                ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        want, _, _, mass, size = ref.decode(k, v, [T], q.double().cpu().numpy(), s.double().cpu().numpy(), np.ones(4), 1.0)
+        e = (d + 8) * 2.0 ** -23 * size
+        err = np.abs(out.double().cpu().numpy() - want)
+        bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass)
+        assert np.all(err <= bound)
