@@ -28,7 +28,8 @@
 // weights relative to a reference of their own, so the V product adds to the output in the MMA itself.  V's reference is
 // a power of two and only rises (to a scale more than kRatio times as large), so the output in its units stays below 2^55:
 // weights of 2^15, codes of 2^9, 2^31 keys.  A unit whose scale is more than kRatio times smaller, or all zeros, gets a
-// product of its own that is added in fp32.
+// product of its own that is added in fp32.  At a warp's end the output is divided by the sum before V's reference is
+// applied, and merging takes weighted means: no answer passes fp32 that V's own numbers do not pass, however many keys.
 //
 // Roundings: q is scaled to fp16 by a power of two per row (bf16 has fewer bits: only
 // elements 2^-25 of the row's largest are lost); the weights 2^(x - m + 8) vscale / vref are rounded to fp16
@@ -74,7 +75,7 @@ struct DecodeArgs {
     unsigned int* status;
     int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
     float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
-    float* part;                         // [2 * grid][R][d]: sums of a run's first / last head
+    float* part;                         // [2 * grid][R][d]: means of a run's first / last head
     float2* part_ml;                     // [2 * grid][R]: their reference and sum
     float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
 };
@@ -439,12 +440,11 @@ __device__ __forceinline__ float row_lse2(float m, float l) { return l == 0.0f ?
 __device__ __forceinline__ int64_t out_row(const DecodeArgs& a, int b, int kvh, int r) {
     return (static_cast<int64_t>(b) * a.n_q + r / a.G) * a.Hq + kvh * a.G + r % a.G;
 }
-// Four outputs of one row: the sums over the warps or parts, divided by the row's sum.
-__device__ __forceinline__ void store_out(__nv_bfloat16* to, float4 o, float l) {
-    const float inv = __fdividef(1.0f, l);   // l < 2^11 * 2^31
-    uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (l == 0.0f) v = make_uint2(0u, 0u);   // no key, or none above -inf
-    *reinterpret_cast<uint2*>(to) = v;
+// 1 / l of a sum of weights (below 2^11 * 2^31); 0 where there is no key, or none above -inf.
+__device__ __forceinline__ float share(float l) { return l == 0.0f ? 0.0f : __fdividef(1.0f, l); }
+// Four outputs of one row.
+__device__ __forceinline__ void store_out(__nv_bfloat16* to, float4 o) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 __device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
     o.x = fmaf(x.x, f, o.x);
@@ -455,7 +455,7 @@ __device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
 
 __device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int kvh, int r, int d, int D, float m, float l,
                                            float4 o) {
-    store_out(a.out + out_row(a, b, kvh, r) * D + d, o, l);
+    store_out(a.out + out_row(a, b, kvh, r) * D + d, o);
     if (d != 0) return;
     const float lse2 = row_lse2(m, l);
     a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + kvh) * kMaxRows + r] = lse2;
@@ -472,8 +472,8 @@ struct Segment {
     int slot;                            // this thread block's part
 };
 
-// A warp's sums of the segment it is in: the warps' parts and the segments are in the same order, so warp w's
-// sums of segment j are entry w + j.
+// A warp's means (o), references and sums of the segment it is in: the warps' parts and the segments are in the same order,
+// so those of warp w and segment j are entry w + j.
 template <int D, int NT>
 struct Shared {
     static constexpr int kW = warps_of(NT);
@@ -482,8 +482,8 @@ struct Shared {
     Segment seg[kW];
     unsigned red[kW], base, next, total;
     int n_seg, b;
-    // what the thread blocks of a cluster hand to the one that finishes a number: their sums and references
-    float4 sums[8 * NT * D / 4 + kMaxCluster];
+    // what the thread blocks of a cluster hand to the one that finishes a number: their means, references and sums
+    float4 means[8 * NT * D / 4 + kMaxCluster];
     float2 ml[kMaxCluster][8 * NT];
 };
 
@@ -501,11 +501,12 @@ __device__ __forceinline__ void keep_sums(const DecodeArgs& a, Shared<D, NT>& sh
                 sh.l[entry][r] = wp.l[nt][c];
             }
             if (r < a.R) {
+                const float part = share(wp.l[nt][c]);
                 float* to = &sh.o[entry][r][D / 8 * wp.g];
 #pragma unroll
                 for (int dm = 0; dm < D / 16; ++dm)
                     *reinterpret_cast<float2*>(to + 2 * dm) =
-                        make_float2(wp.o[dm][nt][c] * vref, wp.o[dm][nt][2 + c] * vref);
+                        make_float2(wp.o[dm][nt][c] * part * vref, wp.o[dm][nt][2 + c] * part * vref);
             }
         }
 }
@@ -519,7 +520,7 @@ __device__ __forceinline__ void store_cluster(void* to, uint32_t rank, float2 v)
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(to, rank)), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Merges the warps' sums of the block's segments: whole heads are done, the others' parts go to the workspace, or, in
+// Merges the warps' means of the block's segments: whole heads are done, the others' parts go to the workspace, or, in
 // a cluster, to the thread block that finishes them (float4 i of the head is block i % cluster's).
 template <int D, int NT>
 __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& sh, int n_seg) {
@@ -529,25 +530,27 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& 
         const int jr = i / (D / 4), j = jr / a.R, r = jr % a.R, d = i % (D / 4) * 4;
         const Segment& sg = sh.seg[j];
         const int e0 = sg.e0, n = sg.e1 - e0;   // n < kW
-        float me[kW], m = kNothing, l = 0.0f;
+        float f[kW], le[kW], m = kNothing, l = 0.0f;
 #pragma unroll
         for (int e = 0; e < kW; ++e) {
-            me[e] = e <= n ? sh.m[e0 + e][r] : kNothing;
-            m = fmaxf(m, me[e]);
+            f[e] = e <= n ? sh.m[e0 + e][r] : kNothing;
+            le[e] = e <= n ? sh.l[e0 + e][r] : 0.0f;
+            m = fmaxf(m, f[e]);
         }
+#pragma unroll
+        for (int e = 0; e < kW; ++e) {
+            f[e] = ex2(f[e] - m);
+            l = fmaf(le[e], f[e], l);
+        }
+        const float part = share(l);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < kW; ++e) {
-            // nothing where a warp saw no key above -inf (one without units has no sums either)
-            const float le = e <= n ? sh.l[e0 + e][r] : 0.0f;
-            if (le == 0.0f) continue;
-            const float f = ex2(me[e] - m);
-            l = fmaf(le, f, l);
-            add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), f);
-        }
+        for (int e = 0; e < kW; ++e)
+            // nothing where a warp saw no key above -inf (one without units has no means either)
+            if (le[e] != 0.0f) add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), le[e] * f[e] * part);
         if (a.cluster > 1) {
             const int v = r * (D / 4) + d / 4, rank = cluster_rank_in(), each = (a.R * (D / 4) - 1) / a.cluster + 1;
-            store_cluster(&sh.sums[rank * each + v / a.cluster], v % a.cluster, o);
+            store_cluster(&sh.means[rank * each + v / a.cluster], v % a.cluster, o);
             if (d / 4 < a.cluster) store_cluster(&sh.ml[rank][r], d / 4, make_float2(m, l));
         } else if (sg.parts == 1) {
             finish_row(a, sg.b, sg.kvh, r, d, D, m, l, o);
@@ -590,13 +593,14 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
                 const int v = i * a.cluster + rank, r = v / (D / 4), d = v % (D / 4) * 4;
                 float m = kNothing, l = 0.0f;
                 for (int p = 0; p < a.cluster; ++p) m = fmaxf(m, sh.ml[p][r].x);
+#pragma unroll 4
+                for (int p = 0; p < a.cluster; ++p) l = fmaf(sh.ml[p][r].y, ex2(sh.ml[p][r].x - m), l);
+                const float part = share(l);
                 float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                 for (int p = 0; p < a.cluster; ++p) {
                     const float2 ml = sh.ml[p][r];
-                    const float f = ex2(ml.x - m);
-                    l = fmaf(ml.y, f, l);
-                    add4(o, sh.sums[p * each + i], f);
+                    add4(o, sh.means[p * each + i], ml.y * ex2(ml.x - m) * part);
                 }
                 finish_row(a, b, kvh, r, d, D, m, l, o);
             }
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
 // Room of a thread block of the second kernel, for either of its tasks.
 constexpr int kMergeVecs = 64, kMergeGroups = kFinThreads / kMergeVecs;   // float4s of the output a thread block merges
 struct MergeRoom {
-    float f[kMaxParts][4], l[4];         // factors and sums of its 2 or 4 rows
+    float f[kMaxParts][4];               // the parts' shares of its 2 or 4 rows
     float4 sum[kMergeGroups][kMergeVecs];
 };
 struct WeightRoom {
@@ -799,16 +803,16 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs& a, MergeRoom& room
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
         for (int y = 0; y < kPer; ++y) {
-            const float f = ex2(ml[y].x - m);
-            l = fmaf(ml[y].y, f, l);
-            if (tid % 32 + 32 * y < np) room.f[tid % 32 + 32 * y][tid / 32] = f;
+            ml[y].y *= ex2(ml[y].x - m);
+            l += ml[y].y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (tid % 32 == 0) {
-            room.l[tid / 32] = l;
-            if (a.lse) a.lse[out_row(a, b, h, row)] = row_lse2(m, l) * kLn2;
-        }
+        const float part = share(l);
+#pragma unroll
+        for (int y = 0; y < kPer; ++y)
+            if (tid % 32 + 32 * y < np) room.f[tid % 32 + 32 * y][tid / 32] = ml[y].y * part;
+        if (tid % 32 == 0 && a.lse) a.lse[out_row(a, b, h, row)] = row_lse2(m, l) * kLn2;
     }
     __syncthreads();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -825,7 +829,7 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs& a, MergeRoom& room
     if (grp == 0 && active) {
 #pragma unroll
         for (int y = 1; y < kMergeGroups; ++y) add4(o, room.sum[y][i], 1.0f);
-        store_out(a.out + out_row(a, b, h, r0 + r) * D + d, o, room.l[r]);
+        store_out(a.out + out_row(a, b, h, r0 + r) * D + d, o);
     }
 }
 

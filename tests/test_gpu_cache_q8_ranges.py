@@ -90,3 +90,40 @@ def test_decode_over_appended_zeros():
         err = np.abs(out.double().cpu().numpy() - want)
         bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass)
         assert np.all(err <= bound)
+
+
+# ------------------------------------------------------------------------------------------- scales of V near fp32's ends
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("e", [100, 110, 117])
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_decode_large_values(fmt, e, launch):
+    """Values near the largest that an append stores: the answer is finite, whatever the keys' number."""
+    B, T, max_len, every = LAUNCHES[launch]
+    lens = [T] * B
+    cache, check, nums, s, w, g = random_cache(fmt, B, T + 5, 1, 64, lens, seed=4)
+    scaled_values(cache, nums, [e - j % 3 for j in range((T + 5) // 32)], lens, fmt)
+    q = torch.randn(B, 1, 3, 64, generator=g).to(torch.bfloat16)
+    check_decode(cache, check, nums, s, w, q, 2 * torch.rand(3, generator=g), 1.2, lens, max_len=max_len)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("scale", [1.5 * 2.0 ** 126, 2.0 ** 127, 1.75 * 2.0 ** 127, 1.25 * 2.0 ** -126, 2.0 ** -130, 2.0 ** -140])
+def test_decode_scales_at_the_ends(fmt, scale):
+    """Any positive finite scale of V, fp32's largest and its subnormals among them (codes such that the values are finite).
+    An answer among bf16's subnormals is half a step of 2^-133 off at most, and the sums' fp32 below 2^-126 a
+    few steps of 2^-149: 2^-133 covers both."""
+    lens = [900]
+    cache, check, nums, s, w, g = random_cache(fmt, 1, 928, 1, 64, lens, seed=6)
+    codes = torch.sign(torch.randn(1, 928, 1, 64, generator=g)) * (1.0 if scale > 1 else 96.0)
+    if scale > 1:
+        codes[:, :, :, ::2] = 0
+    cache.v.copy_(codes.to(ref.DTYPE[fmt]))
+    cache.v_scale.fill_(scale)
+    v = codes.double().numpy() * float(torch.tensor(scale, dtype=torch.float32))
+    q = torch.randn(1, 1, 3, 64, generator=g).to(torch.bfloat16)
+    gain = torch.rand(3, generator=g)
+    out = cache.decode(q.cuda(), gain=gain.cuda(), tau=1.1).double().cpu().numpy()
+    want, _, _, mass, size = ref.decode(nums["k"], v, lens, q.double().numpy(), s.double().numpy(), gain.double().numpy(), 1.1)
+    e = (64 + 8) * 2.0 ** -23 * size
+    bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass) + 2.0 ** -133
+    assert np.all(np.abs(out - want) <= bound)
