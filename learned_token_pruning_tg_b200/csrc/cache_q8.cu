@@ -20,6 +20,7 @@ namespace q8 {
 
 constexpr int kWarps = 4;                // warps of an append or gather thread block (8: 67.5 us for the prompt below)
 constexpr int kReadThreads = 256;
+constexpr float kMostRatio = 262144.0f;  // 2^18 > 448 / 2^-9, the largest and the least code of e4m3 (int8: 128)
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -576,7 +577,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_evict_gather_kernel(const E
         uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
         const float before = __shfl_sync(0xffffffffu, mine, r);
         if (before != scale) {
-            const float ratio = __fdiv_rn(before, scale);
+            // A row with a code other than 0 has before <= qmax / (the least code) scale: below kMostRatio.  One of
+            // zeros may come from any scale, and 0 times an infinite ratio is not 0.
+            const float ratio = fminf(__fdiv_rn(before, scale), kMostRatio);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 float f[4];

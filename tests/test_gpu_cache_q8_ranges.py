@@ -8,7 +8,7 @@ import torch
 
 from learned_token_pruning_tg_b200.cache import KVCacheQ8
 from tests import cache_ref as ref
-from tests.test_gpu_cache_q8 import FORMATS, check_decode, half_step, random_cache
+from tests.test_gpu_cache_q8 import FORMATS, check_decode, guarded_cache, half_step, random_cache, same_numbers
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,27 @@ def test_decode_scales_at_the_ends(fmt, scale):
     e = (64 + 8) * 2.0 ** -23 * size
     bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass) + 2.0 ** -133
     assert np.all(np.abs(out - want) <= bound)
+
+
+# ------------------------------------------------------------------------------------------- eviction of zeros
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 12, 2.0 ** 100])
+def test_evict_rows_of_zeros(fmt, size):
+    """Rows of zeros that leave a block of large numbers: zeros, under the least scale where a new block has no others."""
+    B, T, H, d, budget = 1, 128, 2, 64, 40
+    g = torch.Generator().manual_seed(2)
+    x = (torch.randn(2, B, T, H, d, generator=g) * size).to(torch.bfloat16)
+    keep = torch.arange(1, 2 * budget, 2)
+    x[:, :, keep] = 0
+    x[0, 0, keep[35], 1, 3] = 2.0 ** -100                      # one of the second new block's K rows is not quite zero
+    src, dst = KVCacheQ8(B, T, H, d, fmt=fmt), guarded_cache(fmt, B, 64, H, d)[0]
+    src.lengths.fill_(T)
+    src.append(x[0].cuda(), x[1].cuda())
+    src.w[0, keep] = 1.0
+    nums = [ref.values(ref.code_values(c), sc.double().cpu().numpy()) for c, sc in ((src.k, src.k_scale), (src.v, src.v_scale))]
+    kept = src.evict_into(dst, budget)
+    assert kept[0].tolist() == keep.tolist()
+    for num, codes, scale in zip(nums, (dst.k, dst.v), (dst.k_scale, dst.v_scale)):
+        want, want_scale = ref.append(np.zeros((1, 64, H, d)), np.zeros((1, 2, H)), [budget], [budget], num[:, keep], fmt)
+        same_numbers(codes[:, :budget], want[:, :budget])
+        assert np.array_equal(scale.double().cpu().numpy(), want_scale)
