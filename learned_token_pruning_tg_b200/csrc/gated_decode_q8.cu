@@ -372,7 +372,7 @@ struct Warp {
         }
     }
     __device__ __forceinline__ void values(ValueRegs<D>& v, int blk, int len, const uint32_t (&pf)[2][NT][2],
-                                           float ratio) {
+                                           float ratio, uint32_t& bad) {
         if (FMT == TG_CACHE_E4M3 && (blk + 1) * kBlock > len) {
             // rows behind the sequence may hold anything, NaN codes too: their weight is 0
 #pragma unroll
@@ -382,6 +382,20 @@ struct Warp {
                     if (blk * kBlock + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= len)
 #pragma unroll
                         for (int w = 0; w < D / 32; ++w) v.w[i][j][w] = 0u;
+        }
+        if (FMT == TG_CACHE_E4M3 && unseen(blk, len)) {
+            // nor may a NaN reach the queries that do not see its key (mark_nan sees to the others)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (blk * kBlock + 16 * i + 2 * t + (j & 1) + 8 * (j >> 1) >= len - (a.n_q - 1))
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) {
+                            const uint32_t nan = nan_bytes(v.w[i][j][w]);
+                            bad |= nan;
+                            v.w[i][j][w] &= ~nan;
+                        }
         }
         if (apart(ratio)) {
 #pragma unroll
@@ -396,6 +410,46 @@ struct Warp {
         } else {
 #pragma unroll
             for (int dm = 0; dm < D / 16; ++dm) product(v, dm, pf, o[dm]);
+        }
+    }
+
+    // Whether a block has keys that some query sees and some does not.
+    __device__ __forceinline__ bool unseen(int blk, int len) const {
+        return a.n_q > 1 && (blk + 1) * kBlock > len - (a.n_q - 1);
+    }
+    __device__ __forceinline__ static uint32_t nan_bytes(uint32_t codes) { return __vcmpeq4(codes & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+    // NaN in the outputs of the queries that see a key with a NaN in V, of a block with keys that not all see: where the product
+    // of the NaN codes' places (1 or 0) with what each row sees is not 0.
+    __device__ __forceinline__ void mark_nan(ValueRegs<D>& v, int blk, int len) {
+        const int last = len - blk * kBlock;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = 16 * i + 2 * t + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w)   // e4m3's 1
+                    v.w[i][j][w] = key >= last - (a.n_q - 1) && key < last ? nan_bytes(v.w[i][j][w]) & 0x38383838u : 0u;
+            }
+        uint32_t seen[2][NT][2];             // as B operands: 1 where row 8 nt + g sees the key
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g, end = last - (r < a.R ? a.n_q - 1 - r / a.G : 0) - 2 * t;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    seen[i][nt][k] = (16 * i + 8 * k < end ? 0x3c00u : 0u) | (16 * i + 8 * k + 1 < end ? 0x3c000000u : 0u);
+        }
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm) {
+            float acc[NT][4] = {};
+            product(v, dm, seen, acc);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (acc[nt][c] > 0.0f) o[dm][nt][c] = __int_as_float(0x7fffffff);
         }
     }
 
@@ -414,7 +468,9 @@ struct Warp {
             load_values(v, pv, vs);
         }
         begin(b, kvh);
-        for (int u = u0; u < u1; u += step) {
+        uint32_t bad = 0;
+        int u = u0;
+        for (; u < u1; u += step) {
             uint32_t pf[2][NT][2];
             float ratio;
             scores(k, v.scale, b, kvh, u, len, pf, ratio);
@@ -424,8 +480,19 @@ struct Warp {
             vs += step * a.c.Hkv;
             s += step * kBlock;
             if (u + step < u1) load_keys(k, pk, ks, s);
-            values(v, u, len, pf, ratio);
+            values(v, u, len, pf, ratio, bad);
             if (u + step < u1) load_values(v, pv, vs);
+        }
+        if (FMT == TG_CACHE_E4M3 && __any_sync(0xffffffffu, bad)) {
+            // among the last 2 blocks of the sequence (one that is another warp's may be marked twice)
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                u -= step;
+                if (u < 0 || !unseen(u, len)) continue;
+                load_values(v, a.c.v + b * a.c.ld_seq + (u * static_cast<int64_t>(kBlock) + 2 * t) * a.c.ld_token + kvh * D + g * (D / 8),
+                            a.c.v_scale + (b * a.c.blocks() + u) * a.c.Hkv + kvh);
+                mark_nan(v, u, len);
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

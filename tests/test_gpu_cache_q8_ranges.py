@@ -151,3 +151,32 @@ def test_evict_rows_of_zeros(fmt, size):
         want, want_scale = ref.append(np.zeros((1, 64, H, d)), np.zeros((1, 2, H)), [budget], [budget], num[:, keep], fmt)
         same_numbers(codes[:, :budget], want[:, :budget])
         assert np.array_equal(scale.double().cpu().numpy(), want_scale)
+
+
+# ------------------------------------------------------------------------------------------- NaN of a token not seen
+@pytest.mark.parametrize("launch", LAUNCHES)
+@pytest.mark.parametrize("cut", [5, 30, 3, 0])
+@pytest.mark.parametrize("n_q", [2, 4, 16])
+def test_decode_nan_value_of_an_unseen_token(launch, cut, n_q):
+    """A NaN in V of one of the last tokens gives NaN in its own place of the queries that see the token, and in no other."""
+    B, T, max_len, _ = LAUNCHES[launch]
+    T = T + 5 - cut
+    lens = [T] * B
+    cache, check, nums, s, w, g = random_cache("e4m3", B, T + cut, 1, 64, lens, seed=n_q + cut)
+    places = [(T - 1, 9), (T - max(n_q // 2, 1), 40)]
+    for c, x in places:
+        cache.v.view(torch.uint8)[:, c, 0, x] = 0xff if x == 40 else 0x7f
+        nums["v"][:, c, 0, x] = np.nan
+    q = torch.randn(B, n_q, 1, 64, generator=g).to(torch.bfloat16)
+    gain = torch.ones(1)
+    lse = torch.empty(B, n_q, 1, device="cuda")
+    out = cache.decode(q.cuda(), gain=gain.cuda(), tau=1.2, lse=lse, max_len=max_len).double().cpu().numpy()
+    want, want_lse, _, mass, size = ref.decode(nums["k"], nums["v"], lens, q.double().numpy(), s.double().numpy(),
+                                               gain.double().numpy(), 1.2)
+    nan = np.isnan(want)
+    assert nan[:, -1, 0, 9].all() and not nan[:, 0].any() and nan.any(axis=(1, 2)).sum() == 2 * B
+    assert np.array_equal(np.isnan(out), nan)
+    e = (64 + 8) * 2.0 ** -23 * size
+    bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(np.nan_to_num(want)) + 2.0 ** -10 * np.nan_to_num(mass))
+    assert np.all(np.abs(out - want)[~nan] <= bound[~nan])
+    assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= e + 2.0 ** -20 + 2.0 ** -23 * np.abs(want_lse))
