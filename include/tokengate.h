@@ -491,6 +491,8 @@ tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, t
  * and, with accumulate, cache->w[b, c] += sum over i and h of softmax_c(l_c).
  * A query that sees no key, or none with l_c > -inf, gets out 0 and lse -inf and
  * adds no weight.  Keys with s_c = -inf are masked for heads of positive gain.
+ * l_c is an fp32 number: a row whose keys all have fp32's lowest number as their
+ * bias (gain 1 or less) shares its weight evenly; what is beyond it is -inf.
  * A NaN in a key or value gives NaN to the queries that see it (c < T_i), whatever
  * its bias, and to no other.
  * q, out: [batch, n_q, Hq, d_h] bf16 dense, 16-byte aligned, apart; lse: [batch, n_q,

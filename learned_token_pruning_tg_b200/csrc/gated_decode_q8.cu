@@ -2,8 +2,10 @@
 //
 // With codes K, V and one scale per block of 32 keys and head, for the R = n_q G query
 // rows that read one KV head:
-//   x_rc = (tau / sqrt(d) log2 e) kscale (q_r . K_c) + g_r s_c log2 e      (log2 units)
-//   out_r = sum_blocks vscale sum_{c in block} 2^(x_rc - m_r) V_c / sum_c 2^(x_rc - m_r)
+//   x_rc = (tau / sqrt(d)) kscale (q_r . K_c) + g_r s_c
+//   out_r = sum_blocks vscale sum_{c in block} e^(x_rc - m_r) V_c / sum_c e^(x_rc - m_r)
+// (in natural units, so that a bias of fp32's lowest number, a common mask, stays a number; a weight is
+// 2^((x - m) log2 e), one multiplication more.)
 // The cache is read once: 2 d bytes a key and head, so HBM bounds a long step and latency a
 // short one.
 //
@@ -55,8 +57,8 @@ constexpr int kMaxCluster = 16;
 constexpr int kMaxParts = 160;           // thread blocks of a launch that cuts the units into runs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kShift = 8.0f;           // weights are 2^(x - m + kShift) ...
-constexpr float kLazy = 3.0f;            // ... at most 2^(kShift + kLazy) ...
+constexpr float kShift = 8.0f * kLn2;    // weights are e^(x - m + kShift) ...
+constexpr float kLazy = 3.0f * kLn2;     // ... at most 2^11 ...
 constexpr float kRatio = 16.0f;          // ... times vscale / vref, at most kRatio, and not below 1 / kRatio in a joint product
 constexpr float kNothing = -3.402823466e38f;   // the reference before the first logit
 constexpr int kFinThreads = 256, kWeightKeys = 64, kWeightGroups = kFinThreads / kWeightKeys;
@@ -68,16 +70,16 @@ struct DecodeArgs {
     const float* gain;
     __nv_bfloat16* out;
     float* lse;
-    float scale_log2;                    // tau / sqrt(d) * log2(e)
+    float scale;                         // tau / sqrt(d)
     int n_q, Hq, G, R;
     int Rp;                              // R rounded up to even: a key's logits in the workspace
     int cluster;                         // thread blocks of a head, as one cluster; 0: runs of units
     unsigned int* status;
     int2* heads;                         // [batch * Hkv] first thread block and number of the parts; 0 parts: done
-    float* lse2;                         // [batch * Hkv][kMaxRows], log2 units, of heads that are done
+    float2* rows;                        // [batch * Hkv][kMaxRows] reference and log2 of the sum, of heads that are done
     float* part;                         // [2 * grid][R][d]: means of a run's first / last head
     float2* part_ml;                     // [2 * grid][R]: their reference and sum
-    float* logits;                       // [batch * Hkv][capacity][Rp] log2 units
+    float* logits;                       // [batch * Hkv][capacity][Rp]
 };
 
 // The two halves of a cluster barrier.
@@ -89,6 +91,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+__device__ __forceinline__ float exp_of(float x) { return ex2(x * kLog2e); }
 
 template <int WORDS>
 __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
@@ -139,7 +143,7 @@ struct Warp {
     const DecodeArgs& a;
     const int lane, g, t;
     uint32_t qf[D / 16][NT][2];
-    float f[NT][2], gl2[NT][2];          // logit factor and gain of this lane's query rows 8 nt + 2 t + {0, 1}
+    float f[NT][2], gn[NT][2];          // logit factor and gain of this lane's query rows 8 nt + 2 t + {0, 1}
     float m[NT][2], l[NT][2], o[D / 16][NT][4];   // m: the reference less kShift
     float vinv;                          // o is in units of vref, a power of two; this is its inverse
 
@@ -198,9 +202,9 @@ struct Warp {
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                f[nt][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + i)) * a.scale_log2;
+                f[nt][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + i)) * a.scale;
                 const int rr = 8 * nt + 2 * t + i;
-                gl2[nt][i] = (rr < a.R && a.gain) ? __ldg(a.gain + kvh * a.G + rr % a.G) * kLog2e : 0.0f;
+                gn[nt][i] = (rr < a.R && a.gain) ? __ldg(a.gain + kvh * a.G + rr % a.G) : 0.0f;
                 m[nt][i] = kNothing;
                 l[nt][i] = 0.0f;
             }
@@ -266,7 +270,7 @@ struct Warp {
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        x[i][nt][c] = fmaf(x[i][nt][c], f[nt][c & 1] * k.scale, gl2[nt][c & 1] * k.s[2 * i + (c >> 1)]);
+                        x[i][nt][c] = fmaf(x[i][nt][c], f[nt][c & 1] * k.scale, gn[nt][c & 1] * k.s[2 * i + (c >> 1)]);
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -317,7 +321,7 @@ struct Warp {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     const float mn = fmaxf(m[nt][c], top - kShift);
-                    const float alpha = ex2(m[nt][c] - mn);
+                    const float alpha = exp_of(m[nt][c] - mn);
                     m[nt][c] = mn;
                     l[nt][c] *= alpha;
 #pragma unroll
@@ -349,7 +353,7 @@ struct Warp {
                 float p[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    p[c] = ex2(x[i][nt][c] - m[nt][c & 1]);
+                    p[c] = exp_of(x[i][nt][c] - m[nt][c & 1]);
                     l[nt][c & 1] += p[c];
                 }
                 pf[i][nt][0] = transpose8x8(pack_f16x2(p[0] * f, p[1] * f));
@@ -503,7 +507,9 @@ struct Warp {
     }
 };
 
-__device__ __forceinline__ float row_lse2(float m, float l) { return l == 0.0f ? -INFINITY : m + log2f(l); }
+// The reference and log2 of the sum of a row (infinity where there is no weight), and the row's log-sum-exp.
+__device__ __forceinline__ float2 row_of(float m, float l) { return make_float2(m, l == 0.0f ? INFINITY : log2f(l)); }
+__device__ __forceinline__ float lse_of(float2 row) { return row.y == INFINITY ? -INFINITY : fmaf(row.y, kLn2, row.x); }
 __device__ __forceinline__ int64_t out_row(const DecodeArgs& a, int b, int kvh, int r) {
     return (static_cast<int64_t>(b) * a.n_q + r / a.G) * a.Hq + kvh * a.G + r % a.G;
 }
@@ -524,9 +530,9 @@ __device__ __forceinline__ void finish_row(const DecodeArgs& a, int b, int kvh, 
                                            float4 o) {
     store_out(a.out + out_row(a, b, kvh, r) * D + d, o);
     if (d != 0) return;
-    const float lse2 = row_lse2(m, l);
-    a.lse2[(static_cast<int64_t>(b) * a.c.Hkv + kvh) * kMaxRows + r] = lse2;
-    if (a.lse) a.lse[out_row(a, b, kvh, r)] = lse2 * kLn2;
+    const float2 row = row_of(m, l);
+    a.rows[(static_cast<int64_t>(b) * a.c.Hkv + kvh) * kMaxRows + r] = row;
+    if (a.lse) a.lse[out_row(a, b, kvh, r)] = lse_of(row);
 }
 
 // A thread block's part of one head.
@@ -606,7 +612,7 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& 
         }
 #pragma unroll
         for (int e = 0; e < kW; ++e) {
-            f[e] = ex2(f[e] - m);
+            f[e] = exp_of(f[e] - m);
             l = fmaf(le[e], f[e], l);
         }
         const float part = share(l);
@@ -661,13 +667,13 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
                 float m = kNothing, l = 0.0f;
                 for (int p = 0; p < a.cluster; ++p) m = fmaxf(m, sh.ml[p][r].x);
 #pragma unroll 4
-                for (int p = 0; p < a.cluster; ++p) l = fmaf(sh.ml[p][r].y, ex2(sh.ml[p][r].x - m), l);
+                for (int p = 0; p < a.cluster; ++p) l = fmaf(sh.ml[p][r].y, exp_of(sh.ml[p][r].x - m), l);
                 const float part = share(l);
                 float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                 for (int p = 0; p < a.cluster; ++p) {
                     const float2 ml = sh.ml[p][r];
-                    add4(o, sh.means[p * each + i], ml.y * ex2(ml.x - m) * part);
+                    add4(o, sh.means[p * each + i], ml.y * exp_of(ml.x - m) * part);
                 }
                 finish_row(a, b, kvh, r, d, D, m, l, o);
             }
@@ -829,7 +835,7 @@ struct MergeRoom {
     float4 sum[kMergeGroups][kMergeVecs];
 };
 struct WeightRoom {
-    float lse[64 * kMaxRows];            // infinity in rows that add nothing, the odd last one among them
+    float2 rows[64 * kMaxRows];          // as row_of makes them; the odd last row adds nothing
     float sum[kWeightTiles][kWeightGroups][kWeightKeys];
 };
 
@@ -870,7 +876,7 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs& a, MergeRoom& room
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
         for (int y = 0; y < kPer; ++y) {
-            ml[y].y *= ex2(ml[y].x - m);
+            ml[y].y *= exp_of(ml[y].x - m);
             l += ml[y].y;
         }
 #pragma unroll
@@ -879,7 +885,7 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs& a, MergeRoom& room
 #pragma unroll
         for (int y = 0; y < kPer; ++y)
             if (tid % 32 + 32 * y < np) room.f[tid % 32 + 32 * y][tid / 32] = ml[y].y * part;
-        if (tid % 32 == 0 && a.lse) a.lse[out_row(a, b, h, row)] = row_lse2(m, l) * kLn2;
+        if (tid % 32 == 0 && a.lse) a.lse[out_row(a, b, h, row)] = lse_of(row_of(m, l));
     }
     __syncthreads();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -916,9 +922,9 @@ __device__ __forceinline__ void add_tiles(const DecodeArgs& a, WeightRoom& room,
         for (int i = grp; i < items; i += kWeightGroups) {
             const int h = i / vecs, r = (i - h * vecs) * VEC;
             const float* p = from + h * a.c.capacity * a.Rp + r;
-            float lse[VEC];
+            float2 row[VEC];
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) lse[q] = room.lse[h * a.Rp + r + q];
+            for (int q = 0; q < VEC; ++q) row[q] = room.rows[h * a.Rp + r + q];
 #pragma unroll
             for (int j = 0; j < kWeightTiles; ++j)
                 if (c0 + key + j * stride < len) {
@@ -928,7 +934,7 @@ __device__ __forceinline__ void add_tiles(const DecodeArgs& a, WeightRoom& room,
                     else
                         *reinterpret_cast<float2*>(y) = __ldcg(reinterpret_cast<const float2*>(p + j * stride * a.Rp));
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) sum[j] += ex2(y[q] - lse[q]);
+                    for (int q = 0; q < VEC; ++q) sum[j] += ex2(fmaf(y[q] - row[q].x, kLog2e, -row[q].y));
                 }
         }
 #pragma unroll
@@ -944,7 +950,7 @@ __device__ __forceinline__ void add_tiles(const DecodeArgs& a, WeightRoom& room,
     }
 }
 
-// w[b, c] += sum over heads and rows of 2^(x - lse2), thread block x of nx: 64 keys and 4 groups of heads, up to 4 tiles
+// w[b, c] += sum over heads and rows of e^(x - m) / l, thread block x of nx: 64 keys and 4 groups of heads, up to 4 tiles
 // of keys at once so that many loads are under way, the groups' sums in a fixed order.  The log-sum-exps come from
 // the parts themselves, so that this does not wait for their merging.
 __device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& room, int b, int x, int nx, bool done) {
@@ -954,8 +960,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& roo
         // every head's rows are finished already
         for (int i = tid; i < Hkv * a.Rp; i += kFinThreads) {
             const int h = i / a.Rp, r = i - h * a.Rp;
-            const float v = r < a.R ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : -INFINITY;
-            room.lse[i] = v == -INFINITY ? INFINITY : v;
+            room.rows[i] = r < a.R ? a.rows[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : row_of(0.0f, 0.0f);
         }
     }
     // else 8 lanes a row
@@ -963,7 +968,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& roo
         const int h = i / a.Rp, r = i % a.Rp;
         const bool row = h < Hkv && r < a.R;
         const int2 hd = row ? a.heads[b * Hkv + h] : make_int2(0, 0);
-        float v = row && hd.y == 0 ? a.lse2[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : -INFINITY;
+        float2 v = row && hd.y == 0 ? a.rows[(static_cast<int64_t>(b) * Hkv + h) * kMaxRows + r] : row_of(0.0f, 0.0f);
         float m = kNothing, l = 0.0f;
         for (int p0 = tid % 8; p0 < hd.y; p0 += 32) {
             float2 ml[4];
@@ -973,20 +978,20 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, WeightRoom& roo
                 ml[y] = p < hd.y ? __ldcg(a.part_ml + (2 * (hd.x + p) + (p == 0)) * a.R + r) : make_float2(kNothing, 0.0f);
             }
             const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-            l *= ex2(m - mn);
+            l *= exp_of(m - mn);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) l = fmaf(ml[y].y, ex2(ml[y].x - mn), l);
+            for (int y = 0; y < 4; ++y) l = fmaf(ml[y].y, exp_of(ml[y].x - mn), l);
             m = mn;
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
             const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
             const float mn = fmaxf(m, m2);
-            l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
+            l = l * exp_of(m - mn) + l2 * exp_of(m2 - mn);
             m = mn;
         }
-        if (hd.y) v = row_lse2(m, l);
-        if (tid % 8 == 0 && h < Hkv) room.lse[i] = v == -INFINITY ? INFINITY : v;   // such a row adds nothing
+        if (hd.y) v = row_of(m, l);
+        if (tid % 8 == 0 && h < Hkv) room.rows[i] = v;
     }
     __syncthreads();
     if (a.Rp % 4 == 0)
@@ -1014,17 +1019,17 @@ __global__ void __launch_bounds__(kFinThreads, 4) decode_q8_finish_kernel(const 
         add_weights(a, room.weights, b, x - merges, gridDim.x - merges, merges == 0);
 }
 
-// Workspace: status header, heads, lse2, parts, logits (each from a 256-byte boundary).
+// Workspace: status header, heads, rows, parts, logits (each from a 256-byte boundary).
 struct Layout {
-    size_t heads, lse2, part, part_ml, logits, bytes;
+    size_t heads, rows, part, part_ml, logits, bytes;
 };
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 static Layout layout(const Cache& c, int d_h, int R, bool weights) {
     const int64_t heads = static_cast<int64_t>(c.batch) * c.Hkv;
     Layout L;
     L.heads = kWsHeader;
-    L.lse2 = L.heads + up256(static_cast<size_t>(heads) * 8);
-    L.part = L.lse2 + up256(static_cast<size_t>(heads) * kMaxRows * 4);
+    L.rows = L.heads + up256(static_cast<size_t>(heads) * 8);
+    L.part = L.rows + up256(static_cast<size_t>(heads) * kMaxRows * 8);
     L.part_ml = L.part + up256(static_cast<size_t>(2 * kMaxParts) * R * d_h * 4);
     L.logits = L.part_ml + up256(static_cast<size_t>(2 * kMaxParts) * R * 8);
     L.bytes = L.logits + (weights ? up256(static_cast<size_t>(heads) * c.capacity * ((R + 1) / 2 * 2) * 4) : 0);
@@ -1157,12 +1162,12 @@ extern "C" tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16*
     a.gain = gain;
     a.out = reinterpret_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    a.scale_log2 = tau / std::sqrt(static_cast<float>(cache->d_h)) * q8::kLog2e;
+    a.scale = tau / std::sqrt(static_cast<float>(cache->d_h));
     a.n_q = n_q;
     a.Hq = Hq;
     a.status = status_word(workspace);
     a.heads = reinterpret_cast<int2*>(ws + L.heads);
-    a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
+    a.rows = reinterpret_cast<float2*>(ws + L.rows);
     a.part = reinterpret_cast<float*>(ws + L.part);
     a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
     a.logits = reinterpret_cast<float*>(ws + L.logits);

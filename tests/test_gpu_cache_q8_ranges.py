@@ -180,3 +180,35 @@ def test_decode_nan_value_of_an_unseen_token(launch, cut, n_q):
     bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(np.nan_to_num(want)) + 2.0 ** -10 * np.nan_to_num(mass))
     assert np.all(np.abs(out - want)[~nan] <= bound[~nan])
     assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= e + 2.0 ** -20 + 2.0 ** -23 * np.abs(want_lse))
+
+
+# ------------------------------------------------------------------------------------------- biases of the lowest number
+@pytest.mark.parametrize("gain", [1.0, 0.9, 0.5])
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_decode_rows_of_the_lowest_bias(launch, gain):
+    """Every key biased by fp32's lowest number (a common mask): the logits are finite and equal, so all keys share the
+    weight.  q.k vanishes beside the bias on both sides, so the logits have no error; the rest of the bounds as derived
+    (the sums' fp32 2^-20, a weight 2^-18 of itself)."""
+    B, T, max_len, _ = LAUNCHES[launch]
+    lens = [T - 32 * (b % 3) for b in range(B)]
+    cache, check, nums, s, w, g = random_cache("e4m3", B, T + 5, 1, 64, lens, seed=5)
+    low = torch.finfo(torch.float32).min
+    for b in range(B):
+        s[b, :lens[b]] = low
+    cache.s.copy_(s)
+    w.zero_()
+    cache.w.copy_(w)
+    q = torch.randn(B, 1, 2, 64, generator=g).to(torch.bfloat16)
+    lse = torch.empty(B, 1, 2, device="cuda")
+    out = cache.decode(q.cuda(), gain=torch.full((2,), gain, device="cuda"), lse=lse, accumulate=True, max_len=max_len)
+    n = np.array(lens, dtype=np.float64)[:, None]
+    v = [nums["v"][b, :lens[b], 0] for b in range(B)]
+    want, mass = np.stack([x.mean(0) for x in v])[:, None, None], np.stack([np.abs(x).mean(0) for x in v])[:, None, None]
+    bound = (2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= bound)
+    want_lse = float(torch.tensor(gain)) * low
+    assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= 2.0 ** -23 * abs(want_lse))
+    got = cache.w.double().cpu().numpy()
+    for b in range(B):
+        assert np.all(np.abs(got[b, :lens[b]] - 2 / n[b]) <= 2.0 ** -18 * 2 / n[b])
+    check()
