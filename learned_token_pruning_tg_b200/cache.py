@@ -67,10 +67,11 @@ class KVCacheQ8:
             if self._workspace is None or self._workspace.numel() < n:
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("call reserve() before capturing a decode of this shape")
+                workspace = torch.empty(n, dtype=torch.uint8, device=self.handle.device)
+                workspace[:256].zero_()                     # the status word; the rest is written before it is read
                 if self._workspace is not None:
-                    self._retired.append(self._workspace)   # a captured graph may still use it
-                self._workspace = torch.empty(n, dtype=torch.uint8, device=self.handle.device)
-                self._workspace[:256].zero_()               # the status word; the rest is written before it is read
+                    self._retired.append(self._workspace)   # a captured graph may still use it, and its status stays
+                self._workspace = workspace
             self._room[key] = n
         return self._workspace
 
@@ -106,5 +107,9 @@ class KVCacheQ8:
                                     max_len=max_len)
 
     def device_status(self) -> int:
-        """Raw TG_STATUS_* bits of the calls so far (synchronises)."""
-        return tg.tg_device_status(self._workspace)
+        """Raw TG_STATUS_* bits of the calls so far, graphs captured on an earlier workspace among them (synchronises)."""
+        status = 0
+        with torch.cuda.device(self.handle.device):
+            for workspace in (*self._retired, self._workspace):
+                status |= tg.tg_device_status(workspace)
+        return status

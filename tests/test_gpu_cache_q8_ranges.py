@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from learned_token_pruning_tg_b200 import tokengate as tg
 from learned_token_pruning_tg_b200.cache import KVCacheQ8
 from tests import cache_ref as ref
 from tests.test_gpu_cache_q8 import FORMATS, check_decode, guarded_cache, half_step, random_cache, same_numbers
@@ -212,3 +213,33 @@ def test_decode_rows_of_the_lowest_bias(launch, gain):
     for b in range(B):
         assert np.all(np.abs(got[b, :lens[b]] - 2 / n[b]) <= 2.0 ** -18 * 2 / n[b])
     check()
+
+
+# ------------------------------------------------------------------------------------------- status
+def test_status_of_earlier_calls_stays():
+    """What an append flagged is still there when a decode has made the workspace larger, and when a graph captured on the
+    smaller one runs once more."""
+    cache = KVCacheQ8(1, 64, 1, 64)
+    x = torch.ones(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    bad = x.clone()
+    bad[..., 3] = float("inf")
+    cache.lengths.fill_(1)
+    cache.append(bad, x)
+    q = torch.ones(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cache.decode(q)
+    assert cache.device_status() == tg.TG_STATUS_CACHE_VALUE
+    cache.decode(q, accumulate=True)
+    assert cache.device_status() == tg.TG_STATUS_CACHE_VALUE
+
+    cache = KVCacheQ8(1, 64, 1, 64)
+    cache.lengths.fill_(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.append(x, x)
+    cache.decode(q)
+    assert cache.device_status() == 0
+    cache.lengths.fill_(65)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert cache.device_status() == tg.TG_STATUS_CACHE_LENGTH
