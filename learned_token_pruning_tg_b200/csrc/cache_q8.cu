@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_q8_kernel(const ReadA
     int64_t rows = __ldg(a.c.lengths + b) - a.first;
     if (rows > a.n) rows = a.n;          // (first + n <= capacity)
     rows = rows - row0 < a.tokens ? rows - row0 : a.tokens;
+    if (rows <= 0) return;               // (a length far below 0 does not fit an int here)
     const int per_row = a.c.Hkv * (D / 8), items = static_cast<int>(rows) * per_row;
     for (int i = threadIdx.x; i < items; i += kReadThreads) {
         const int r = i / per_row, col = (i - r * per_row) * 8;

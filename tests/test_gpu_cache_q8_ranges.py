@@ -9,7 +9,7 @@ import torch
 from learned_token_pruning_tg_b200 import tokengate as tg
 from learned_token_pruning_tg_b200.cache import KVCacheQ8
 from tests import cache_ref as ref
-from tests.test_gpu_cache_q8 import FORMATS, check_decode, guarded_cache, half_step, random_cache, same_numbers
+from tests.test_gpu_cache_q8 import FORMATS, check_decode, guarded_cache, half_step, ints, random_cache, same_numbers
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +243,17 @@ def test_status_of_earlier_calls_stays():
     graph.replay()
     torch.cuda.synchronize()
     assert cache.device_status() == tg.TG_STATUS_CACHE_LENGTH
+
+
+# ------------------------------------------------------------------------------------------- lengths
+def test_read_with_the_lowest_length():
+    """A length of int32's lowest number reads nothing, from wherever the read begins."""
+    cache, check, nums, s, w, g = random_cache("int8", 2, 320, 2, 64, [300, 300], seed=1)
+    cache.lengths.copy_(ints([-2 ** 31, 300]))
+    for first in (0, 1, 64):
+        out = [torch.full((2, 320 - first, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        cache.read(*out, first=first)
+        torch.cuda.synchronize()
+        check()
+        assert bool((out[0][0] == 7).all()) and bool((out[1][0] == 7).all())
+        assert np.array_equal(out[0][1, :300 - first].double().cpu().numpy(), nums["k"][1, first:300])
