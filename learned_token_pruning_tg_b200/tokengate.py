@@ -473,6 +473,23 @@ def tg_gated_decode(q, k_cache, v_cache, out, workspace, s_cache=None, gain=None
     return out
 
 
+def _cache_strides(k, v):
+    """Token and sequence stride of a cache's codes [B, capacity, Hkv, d_h], K and V of one shape."""
+    B, cap, Hkv, d_h = k.shape
+    row = Hkv * d_h
+    if k.numel() == 0:
+        return row, cap * row
+    # strides of dimensions of one entry say nothing
+    strides, other = ([st if n > 1 else None for st, n in zip(t.stride(), t.shape)] for t in (k, v))
+    if strides != other or strides[3] != 1 or strides[2] not in (None, d_h):
+        raise ValueError("k and v must have equal strides and heads dense in a token")
+    ld_token = row if strides[1] is None else strides[1]
+    ld_seq = cap * ld_token if strides[0] is None else strides[0]
+    if ld_token < row or ld_seq < (cap - 1) * ld_token + row:
+        raise ValueError("a cache's tokens must follow one another, and its sequences (neither expanded nor interleaved)")
+    return ld_token, ld_seq
+
+
 class CacheQ8:
     """An 8-bit KV cache as the tg_cache_* calls and tg_gated_decode_q8 take it: the checked tensors and
     the C struct that points to them.
@@ -500,14 +517,7 @@ class CacheQ8:
         for t in (v, k_scale, v_scale, lengths, s, w):
             if t is not None and t.device != k.device:
                 raise ValueError("a cache's tensors must be on one device")
-        ld_token, ld_seq = Hkv * d_h, cap * Hkv * d_h
-        if k.numel():
-            # strides of dimensions of one entry say nothing
-            strides = [tuple(st if n > 1 else None for st, n in zip(t.stride(), t.shape)) for t in (k, v)]
-            if strides[0] != strides[1] or strides[0][3] != 1 or strides[0][2] not in (None, d_h):
-                raise ValueError("k and v must have equal strides and heads dense in a token")
-            ld_token = strides[0][1] or ld_token
-            ld_seq = strides[0][0] or cap * ld_token
+        ld_token, ld_seq = _cache_strides(k, v)
         self.k, self.v, self.k_scale, self.v_scale, self.lengths, self.s, self.w = k, v, k_scale, v_scale, lengths, s, w
         self.batch, self.capacity, self.Hkv, self.d_h, self.format, self.device = B, cap, Hkv, d_h, fmt, k.device
         self.index = k.get_device()
