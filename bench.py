@@ -843,7 +843,8 @@ def run_decode(args, rank, world, local_rank):
             "dtype": args.cache, "data": "synthetic (seeded random caches)",
             "config": {"workload": f"{cfg.name} decode", "cache": args.cache, "layers": cfg.n_layers, "gate_layer": L,
                        "keys_per_layer": {"up_to_gate": T_all, "above_gate": T_kept}, "Hq": Hq, "Hkv": Hkv,
-                       "d_h": d_h, "timing": "one CUDA graph of the 28 launches per step, replayed"},
+                       "d_h": d_h, "timing": "one CUDA graph of the 28 layers' calls per step, replayed",
+                       "launches": "a call over a long 8-bit cache is two, counted as one"},
             "impl": "tokengate", "dense_ms": ms_dense, "speedup": ms_dense / ms_pruned,
             "bytes_per_step": {"pruned": b_pruned, "dense": b_dense},
             "roofline": {"bound": "hbm", "achieved": achieved, "peak": peaks["hbm_gbs"], "unit": "GB/s",
@@ -855,9 +856,14 @@ def run_decode(args, rank, world, local_rank):
                                   d_h, 1e3, "ms")}
 
 
+def caches_in_turn(nbytes):
+    """How many caches of this size a timed loop goes through, so that what it reads is at least twice the L2."""
+    return max(1, -(-2 * L2_BYTES // nbytes))
+
+
 def run_decode_layer(args, rank, world, local_rank):
     """One layer's decoding-step attention over a 64k cache (65,537 keys x 8 KV heads x 128, K and V
-    268 MB, above L2): the single launch the decode kernel's ncu summary captures."""
+    268 MB in bf16; two caches of 135 MB in turn in 8 bits): the launch the decode kernels' ncu summaries capture."""
     from learned_token_pruning_tg_b200 import stack as stk
     from learned_token_pruning_tg_b200 import tokengate as tg
     dev = torch.device("cuda", local_rank)
@@ -866,25 +872,29 @@ def run_decode_layer(args, rank, world, local_rank):
     T = cfg.N + 1
     gen = torch.Generator(device=dev)
     gen.manual_seed(cfg.seed + 11 + rank)
-    layer = DecodeLayerCache(args.cache, T, cfg.Hq, cfg.Hkv, cfg.d_h, gen, dev)
+    layers = [DecodeLayerCache(args.cache, T, cfg.Hq, cfg.Hkv, cfg.d_h, gen, dev)]
+    nbytes = layers[0].bytes + layers[0].score_bytes
+    layers += [DecodeLayerCache(args.cache, T, cfg.Hq, cfg.Hkv, cfg.d_h, gen, dev) for _ in range(caches_in_turn(nbytes) - 1)]
     q = torch.randn(cfg.Hq, cfg.d_h, generator=gen, device=dev, dtype=torch.bfloat16)
     gain = 2.0 * torch.rand(cfg.Hq, generator=gen, device=dev)
     out = torch.empty(cfg.Hq, cfg.d_h, dtype=torch.bfloat16, device=dev)
     ws = tg.new_workspace(0, cfg.Hq, op=tg.TG_OP_DECODE, device=dev)
-    for _ in range(max(3, args.warmup)):
-        layer.decode(q, out, ws, gain=gain, tau=1.1)
+    for i in range(max(3, args.warmup)):
+        layers[i % len(layers)].decode(q, out, ws, gain=gain, tau=1.1)
     torch.cuda.synchronize()
     reps = max(3, min(args.steps, 100))
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     e0.record()
-    for _ in range(reps):
-        layer.decode(q, out, ws, gain=gain, tau=1.1)
+    for i in range(reps):
+        layers[i % len(layers)].decode(q, out, ws, gain=gain, tau=1.1)
     e1.record()
     torch.cuda.synchronize()
     us = reduce_max(e0.elapsed_time(e1) / reps * 1e3, dev)
     if rank != 0:
         return None
-    nbytes = layer.bytes + layer.score_bytes
+    status = tg.tg_device_status(ws)
+    for layer in layers:
+        status |= layer.status()
     peaks = load_peaks()
     gbs = nbytes / (us * 1e-6) / 1e9
     return {"metric": "one layer's decoding-step attention over a 64k KV cache", "value": us, "unit": "us",
@@ -892,12 +902,13 @@ def run_decode_layer(args, rank, world, local_rank):
             "higher_is_better": False, "scaling": "weak", "vs_baseline": None, "dtype": args.cache,
             "data": "synthetic (seeded random cache)",
             "config": {"workload": "qwen3-1.7b 64k layer cache", "cache": args.cache, "T": T, "Hq": cfg.Hq, "Hkv": cfg.Hkv, "d_h": cfg.d_h,
-                       "l2": f"cache {nbytes / 1e6:.0f} MB > L2, no flush"},
+                       "l2": f"{len(layers)} cache(s) of {nbytes / 1e6:.0f} MB in turn > 2 x 126 MB L2, no flush",
+                       "launches": "a call over an 8-bit cache this long is two, counted as one"},
             "impl": "tokengate",
             "roofline": {"bound": "hbm", "achieved": gbs, "peak": peaks["hbm_gbs"], "unit": "GB/s",
                          "frac": gbs / peaks["hbm_gbs"], "traffic": None,
                          "kernel": "gated_decode_kernel" if args.cache == "bf16" else "gated_decode_q8_kernel"},
-            "gpu_launches": reps, "device_status": tg.tg_device_status(ws) | layer.status(),
+            "gpu_launches": reps, "device_status": status,
             **decode_cpu_baseline(args, [T], cfg.Hq, cfg.Hkv, cfg.d_h, 1e6, "us")}
 
 
