@@ -504,7 +504,8 @@ tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, t
  * accumulate.  Every code is read once (HBM-bound); logits, softmax
  * and sums in fp32, the products on the tensor cores from the codes in fp16
  * (exact) with q scaled by a power of two to fp16 and the softmax's weights
- * rounded to fp16.  Deterministic. */
+ * rounded to fp16 (those below 2^-18 of a row's largest in steps of 2^-28 of it).
+ * Finite logits over values within bf16's range give a finite out.  Deterministic. */
 tg_status tg_gated_decode_q8(const tg_cache_q8* cache, const tg_bf16* q, int32_t n_q, int32_t Hq, const float* gain,
                              float tau, int32_t accumulate, int64_t max_len, tg_bf16* out, float* lse,
                              void* workspace, size_t workspace_bytes, void* stream);

@@ -6,11 +6,11 @@
 //
 // append: bf16 rows (2 rows a warp load, 16 bytes a lane) -> codes (8 bytes a lane).  A block with tokens of an
 //   earlier append keeps the larger scale; its codes move to it by one multiplication with a power
-//   of two and one rounding.  HBM bounds a prompt: 65536 tokens of 8 heads of 128 (403 MB) take 63.3 us, 6.4 TB/s;
-//   one token is a launch (3 us in a graph).
+//   of two and one rounding.  HBM bounds a prompt: 65536 tokens of 8 heads of 128 (403 MB) take 63.5 us, 6.4 TB/s
+//   (replayed in a graph; 67 us as calls one by one); one token is a launch (2.6 us in a graph).
 // evict: one thread block, or a cluster of them, finds a sequence's kept slots by a radix select over the
 //   weights (11 + 11 + 10 bits of the order-preserving key), then one warp per new block gathers its 32 rows.
-//   Latency bounds both: 8961 tokens to 8704 (36 MB) 20.5 us, 65537 to 8704 25 us, half of either the select.
+//   Latency bounds both: 8961 tokens to 8704 (36 MB) 20.4 us, 65537 to 8704 23.3 us, half of either the select.
 //   (4 rows, or 1, a lane instead of 8: 1.0 and 1.8 us more.)
 // read: HBM or L2 bounds it (24 MB of ragged sequences in about 6 us).
 #include "tg_cache.cuh"

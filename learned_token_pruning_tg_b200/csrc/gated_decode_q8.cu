@@ -34,14 +34,15 @@
 // applied, and merging takes weighted means: no answer passes fp32 that V's own numbers do not pass, however many keys.
 //
 // Roundings: q is scaled to fp16 by a power of two per row (bf16 has fewer bits: only
-// elements 2^-25 of the row's largest are lost); the weights 2^(x - m + 8) vscale / vref are rounded to fp16
+// elements 2^-25 of the row's largest are lost); the weights 2^8 e^(x - m) vscale / vref are rounded to fp16
 // for the V product (2^-12 each, below the output's bf16; at most 2^15, and those under 2^-18 of the reference in
-// steps of 2^-28 of it, so that 2^17 such keys together stay below 2^-12), their sum is not.
+// steps of 2^-28 of it, so that 2^17 such keys together stay below 2^-12; it shows where their V is 2^18 times that of the
+// keys that the row attends to), their sum is not.
 //
-// Measured (one B200, 8 KV heads of 128, 2 query heads each): 65537 keys 32.1 us, 4.2 TB/s of the 6.55 a copy reaches;
+// Measured (one B200, 8 KV heads of 128, 2 query heads each): 65537 keys 32.8 us, 4.1 TB/s of the 6.55 a copy reaches;
 // about 10 us of every long step are fixed (launch and lengths 2.5, first loads 1.5, the last unit and the merge 2.5,
 // the second kernel 3.7), the loads alone run at 5.8 TB/s, and the arithmetic without them takes half their time.  Two
-// sequences of 131073 keys 93 us, 5.8 TB/s.  8705 keys 11.8 us (a cluster a head), 15.1 us with the weights.
+// sequences of 131073 keys 92.5 us, 5.8 TB/s.  8705 keys 11.8 us (a cluster a head), 15.2 us with the weights.
 #include <cmath>
 
 #include "tg_cache.cuh"
@@ -1070,10 +1071,13 @@ static int max_clusters(int cl) {
 
 // Thread blocks of a head: the fewest that give a warp no more units than the most whose clusters all run at the same
 // time would, one unit where that many fit; 0 (runs of units) where a warp would have more than 2 units in a thread
-// block alone, or 4 in a cluster.  Returns -1 where the kernel cannot be set up.  Measured, cluster against runs, in
-// us: 8 heads of 2 rows, 1025 keys 8.0 (3) to 9.7, 8705 keys 11.5 to 13.1, 12289 keys 13.2 to 14.1; one head of 8 rows,
-// 8705 keys 9.9 (12) to 15.1; 16 heads of 2 rows, 4097 keys 10.2 to 13.3, 8705 keys 13.8 to 16.6.  Sizes that are powers
-// of two alone: 16 heads, 2049 keys 9.7 to 7.9, 8705 keys 16.6 to 13.8; 8 heads as they are.
+// block alone, or 4 in a cluster.  Returns -1 where the kernel cannot be set up.  Measured, e4m3 without weights, cluster
+// against runs in us (* the side that the rule takes):
+//   keys                       1025       2049        4097         8705        12289        16385        24577        65537
+//   8 heads of 2 rows      *7.7  9.4  *7.3  9.9   *9.5 10.1   *11.3 12.5   *13.6 14.7   *16.3 16.1   20.6 *19.0   40.0 *32.6
+//   16 heads of 2 rows     *7.9 10.1  *7.7 10.3  *10.6 13.4   *14.9 17.3   19.0 *19.8   22.8 *21.9   28.8 *26.8   62.5 *52.5
+//   one head of 8 rows     *7.9  9.4  *7.5 10.4   *8.1 13.3    *9.6 13.0   *11.0 13.2   *11.3 13.4   14.1 *13.7   25.0 *17.3
+// (16 heads over 2049 keys take 9.7 us where only powers of two are allowed as a cluster's size.)
 template <int D, int FMT, int NT, bool kWeights>
 static int cluster_for(int64_t heads, int64_t blocks) {
     static std::atomic<int> smem_set[64];
