@@ -494,7 +494,7 @@ tg_status tg_cache_read_q8(const tg_cache_q8* cache, int64_t first, int64_t n, t
  * l_c is an fp32 number: a row whose keys all have fp32's lowest number as their
  * bias (gain 1 or less) shares its weight evenly; what is beyond it is -inf.
  * A NaN in a key or value gives NaN to the queries that see it (c < T_i), whatever
- * its bias, and to no other.
+ * its bias (a mask takes its weight, and 0 times NaN is NaN), and to no other.
  * q, out: [batch, n_q, Hq, d_h] bf16 dense, 16-byte aligned, apart; lse: [batch, n_q,
  * Hq] fp32 or NULL.  The bias is 0 where cache->s or gain is NULL.
  * max_len: an upper bound on lengths that sizes the launch (0 = capacity);

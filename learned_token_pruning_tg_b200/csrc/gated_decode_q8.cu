@@ -605,10 +605,12 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& 
         const Segment& sg = sh.seg[j];
         const int e0 = sg.e0, n = sg.e1 - e0;   // n < kW
         float f[kW], le[kW], m = kNothing, l = 0.0f;
+        unsigned live = 0;                   // the warps with units: the others left no means
 #pragma unroll
         for (int e = 0; e < kW; ++e) {
-            f[e] = e <= n ? sh.m[e0 + e][r] : kNothing;
+            f[e] = e <= n ? sh.m[e0 + e][r] : -INFINITY;
             le[e] = e <= n ? sh.l[e0 + e][r] : 0.0f;
+            live |= f[e] == -INFINITY ? 0u : 1u << e;
             m = fmaxf(m, f[e]);
         }
 #pragma unroll
@@ -620,8 +622,8 @@ __device__ __forceinline__ void merge_warps(const DecodeArgs& a, Shared<D, NT>& 
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < kW; ++e)
-            // nothing where a warp saw no key above -inf (one without units has no means either)
-            if (le[e] != 0.0f) add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), le[e] * f[e] * part);
+            // (a warp that saw no key above -inf adds 0, or the NaN of a value: every launch gives the same)
+            if (live >> e & 1u) add4(o, *reinterpret_cast<const float4*>(&sh.o[e0 + e][r][d]), le[e] * f[e] * part);
         if (a.cluster > 1) {
             const int v = r * (D / 4) + d / 4, rank = cluster_rank_in(), each = (a.R * (D / 4) - 1) / a.cluster + 1;
             store_cluster(&sh.means[rank * each + v / a.cluster], v % a.cluster, o);
@@ -789,7 +791,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) gated_decode_q8_kernel(c
             const unsigned x_end = units * (warp + 1) / kW;
             int j = 0;
             while (j + 1 < sh.n_seg && x >= sh.seg[j].to) ++j;
-            if (x == x_end && lane < 8 * NT) sh.m[warp + j][lane] = kNothing, sh.l[warp + j][lane] = 0.0f;
+            if (x == x_end && lane < 8 * NT) sh.m[warp + j][lane] = -INFINITY, sh.l[warp + j][lane] = 0.0f;
             for (; x < x_end; ++j) {
                 const Segment& sg = sh.seg[j];
                 const unsigned stop = min(sg.to, x_end);

@@ -257,3 +257,30 @@ def test_read_with_the_lowest_length():
         check()
         assert bool((out[0][0] == 7).all()) and bool((out[1][0] == 7).all())
         assert np.array_equal(out[0][1, :300 - first].double().cpu().numpy(), nums["k"][1, first:300])
+
+
+# ------------------------------------------------------------------------------------------- NaN of a masked token
+@pytest.mark.parametrize("rest", [True, False])
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_decode_nan_value_of_a_masked_token(launch, rest):
+    """A NaN in V of a key that a bias of -inf masks is a NaN in its place (0 times NaN), whichever keys share its warp:
+    among masked keys all around it, with other keys (rest) or none that count."""
+    B, T, max_len, _ = LAUNCHES[launch]
+    lens = [T] * B
+    cache, check, nums, s, w, g = random_cache("e4m3", B, T + 5, 1, 64, lens, seed=9)
+    s[:, T // 4: T] = float("-inf")
+    if not rest:
+        s[:, :T] = float("-inf")
+    cache.s.copy_(s)
+    at = T // 2 + 3
+    cache.v.view(torch.uint8)[:, at, 0, 21] = 0x7f
+    q = torch.randn(B, 1, 3, 64, generator=g).to(torch.bfloat16)
+    out = cache.decode(q.cuda(), gain=torch.full((3,), 0.8, device="cuda"), tau=1.2, max_len=max_len).double().cpu().numpy()
+    nan = np.zeros(out.shape, dtype=bool)
+    nan[..., 21] = True
+    assert np.array_equal(np.isnan(out), nan)
+    want, _, _, mass, size = ref.decode(nums["k"], nums["v"], lens, q.double().numpy(), s.double().numpy(), np.full(3, np.float32(0.8)), 1.2)
+    e = (64 + 8) * 2.0 ** -23 * size
+    bound = (2 * e + 2.0 ** -12 + 2.0 ** -19) * mass * (1 + 2.0 ** -8) + half_step(np.abs(want) + 2.0 ** -10 * mass)
+    assert np.all(np.abs(out - want)[~nan] <= bound[~nan])
+    assert rest or not out[~nan].any()
